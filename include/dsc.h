@@ -491,6 +491,129 @@ DSC_API dsc_status dsc_lowrank_decode(void *stream, int dtype, int64_t B, int64_
 DSC_API dsc_status dsc_state_from_prefill(void *stream, int dtype, int64_t B, int64_t T, int64_t D, int32_t W,
                                   const void *x, const int32_t *cu_seqlens, int32_t n_seqs, void *state);
 
+/*
+ * Attention and its cache: what a block does with the layer's output.  The
+ * pages put the layer on the Q, K and V projections right before the rotary
+ * embedding and attention (Methodology, "placement"), so a token's row is
+ * [Q | K | V]: Hq query heads, Hkv key heads and Hkv value heads of head_dim
+ * channels.  The calls below take q, k and v as rows of any such tensor:
+ *   X_stride   elements from one token's row to the next, >= heads*head_dim,
+ *              <= 2^20, a multiple of 8 (bf16) / 4 (fp32); q, k, v may be
+ *              views of one (N, (Hq + 2 Hkv) head_dim) tensor, and so may dq,
+ *              dk, dv of another (outputs that interleave without sharing a
+ *              byte do not overlap).
+ *   Hq, Hkv    Hq a multiple of Hkv; query head a reads key head a/(Hq/Hkv).
+ *   head_dim   a multiple of 8 (bf16) / 4 (fp32), at most 128
+ *              (DSC_ERR_UNSUPPORTED otherwise).
+ *   scale      factor of the scores, positive and finite (usually
+ *              1/sqrt(head_dim)).
+ * Scores, softmax statistics and sums are fp32; with DSC_BF16 the
+ * probabilities and score gradients are rounded to bf16 as operands of the
+ * matrix cores, and each output once.  These calls also take offsets that
+ * are equal (sequences without tokens).
+ */
+
+/*
+ * Causal attention over whole prompts.  For token i of a sequence and query
+ * head a with key head b:
+ *   s_ij = scale * <q[i,a], k[j,b]>  for the tokens j <= i of i's sequence,
+ *   lse[a,i] = log sum_j exp(s_ij),   o[i,a] = sum_j exp(s_ij - lse[a,i]) v[j,b].
+ *
+ *   q (B*T rows of Hq heads), k, v (B*T rows of Hkv heads) dtype, in.
+ *   o (B,T,Hq,head_dim) dtype, out, dense.
+ *   lse (Hq, B*T) fp32, out; NULL when not wanted (the backward needs it).
+ *   cu_seqlens, n_seqs as above.  Tokens outside a row's sequence and after
+ *   it do not enter its result, whatever they hold.
+ */
+DSC_API dsc_status dsc_attn_fwd(void *stream, int dtype, int64_t B, int64_t T, int32_t Hq, int32_t Hkv,
+                                int32_t head_dim, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                                const void *v, int64_t v_stride, const int32_t *cu_seqlens, int32_t n_seqs,
+                                float scale, void *o, float *lse);
+
+/* Bytes of device workspace dsc_attn_bwd needs (0 for invalid sizes): two
+ * fp32 values per query head and token. */
+DSC_API size_t dsc_attn_bwd_workspace_size(int dtype, int64_t B, int64_t T, int32_t Hq, int32_t Hkv,
+                                           int32_t head_dim);
+
+/*
+ * Backward of dsc_attn_fwd for L = <dout, o>.  With p_ij = exp(s_ij - lse_i),
+ * delta_i = <dout_i, o_i> and ds_ij = scale * p_ij (<dout_i, v_j> - delta_i):
+ *   dq_i = sum_j ds_ij k_j,   dk_j = sum_i ds_ij q_i,   dv_j = sum_i p_ij dout_i,
+ * dk and dv summed over the query heads of the group.  Every sum has one
+ * fixed order: equal inputs give bitwise equal gradients.
+ *
+ *   q, k, v, cu_seqlens, scale as given to the forward, o and lse its outputs;
+ *   dout (B,T,Hq,head_dim) dtype, in, dense.  dq, dk, dv dtype, out, rows
+ *   like q, k, v with strides of their own.  workspace: at least
+ *   dsc_attn_bwd_workspace_size() bytes, 16-byte aligned, contents undefined
+ *   on entry and exit, overlapping no argument.
+ */
+DSC_API dsc_status dsc_attn_bwd(void *stream, int dtype, int64_t B, int64_t T, int32_t Hq, int32_t Hkv,
+                                int32_t head_dim, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                                const void *v, int64_t v_stride, const void *o, const float *lse, const void *dout,
+                                const int32_t *cu_seqlens, int32_t n_seqs, float scale, void *dq, int64_t dq_stride,
+                                void *dk, int64_t dk_stride, void *dv, int64_t dv_stride, void *workspace,
+                                size_t workspace_bytes);
+
+/*
+ * New tokens' keys and values into a paged cache, with the rotary embedding
+ * (dsc_rope_table's) of the keys, and of the queries, on the way.
+ *
+ *   k_cache, v_cache  (num_pages, Hkv, page_size, head_dim) dtype, updated in
+ *              place: only the new tokens' places are written.
+ *   page_table (n_seqs, max_pages) int32, in, device: position p of sequence s
+ *              lives on page page_table[s, p / page_size] at p % page_size.
+ *   cu_seqlens NULL: one new token per sequence (N == n_seqs, a decoding
+ *              step).  Otherwise int32[n_seqs+1] offsets of each sequence's
+ *              new tokens among the N (a prefill); a sequence may have none.
+ *   start      (n_seqs,) int32, in, device: tokens sequence s already has in
+ *              the cache; new token i of the sequence takes position
+ *              start[s] + i.
+ *   k, v (N rows of Hkv heads) in.  q (N rows of Hq heads) in and q_out
+ *   (N, Hq, head_dim) out, dense: the rotated queries; both NULL for keys and
+ *   values only (Hq is then only checked).
+ *   table      (max_pos, head_dim/2, 2) fp32 from dsc_rope_table, or NULL for
+ *              rows that are rotated already (dsc_headwise_rope_*,
+ *              dsc_lowrank_rope_*): keys and queries are then copied.
+ * A token whose position lies outside the page table, or whose page number
+ * lies outside the pool, is not written; a position without a table row
+ * (>= max_pos) turns to NaN.  Two tokens with one place leave either.
+ */
+DSC_API dsc_status dsc_kv_append(void *stream, int dtype, int64_t N, int32_t n_seqs, int32_t Hq, int32_t Hkv,
+                                 int32_t head_dim, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                                 const void *v, int64_t v_stride, const int32_t *cu_seqlens, const int32_t *start,
+                                 const float *table, int64_t max_pos, void *k_cache, void *v_cache,
+                                 int64_t num_pages, int32_t page_size, const int32_t *page_table, int64_t max_pages,
+                                 void *q_out);
+
+/* Bytes of device workspace dsc_attn_decode needs for these sizes (0 when
+ * none, and for invalid sizes): partial rows of the chunks that the length is
+ * cut into. */
+DSC_API size_t dsc_attn_decode_workspace_size(int dtype, int64_t S, int32_t Hq, int32_t Hkv, int32_t head_dim,
+                                              int32_t page_size, int64_t max_pages);
+
+/*
+ * Attention of one new token per sequence over the paged cache:
+ *   o[s,a] = sum_{t < lens[s]} p_t v_t,   p = softmax_t(scale * <q[s,a], k_t>),
+ * k_t, v_t the cached rows of query head a's key head (the new token's own
+ * among them: append first, then lens[s] counts it).
+ *
+ *   q (S rows of Hq heads) in.  o (S, Hq, head_dim) dtype, out, dense.
+ *   k_cache, v_cache, page_table as dsc_kv_append, in.
+ *   lens (S,) int32, in, device: 0..max_pages*page_size; 0 gives a zero row.
+ *              A length outside that range, or a page number outside the pool
+ *              within it, gives NaN.  What pages hold past the length does not
+ *              enter.
+ *   S*Hq at most 2^20.  workspace as sized above, 16-byte aligned, contents
+ *   undefined on entry and exit, overlapping no argument (may be NULL when
+ *   the size is 0).  The sums have one fixed order for given sizes.
+ */
+DSC_API dsc_status dsc_attn_decode(void *stream, int dtype, int64_t S, int32_t Hq, int32_t Hkv, int32_t head_dim,
+                                   const void *q, int64_t q_stride, const void *k_cache, const void *v_cache,
+                                   int64_t num_pages, int32_t page_size, const int32_t *page_table,
+                                   int64_t max_pages, const int32_t *lens, float scale, void *o, void *workspace,
+                                   size_t workspace_bytes);
+
 /* Static name of a status code. */
 DSC_API const char *dsc_status_string(int status);
 

@@ -69,6 +69,17 @@ def lib() -> ctypes.CDLL:
         L.dsc_headwise_gen_bwd.argtypes = [p, i, i64, i64, i64, i32, i32, i64, p, p, p, p, p, i32, i32, p, p, p,
                                            p, ctypes.c_size_t]
         L.dsc_generate_filters.argtypes = [p, i, i64, i64, i64, p, p, p]
+        f32, sz = ctypes.c_float, ctypes.c_size_t
+        L.dsc_attn_fwd.argtypes = [p, i, i64, i64, i32, i32, i32, p, i64, p, i64, p, i64, p, i32, f32, p, p]
+        L.dsc_attn_bwd_workspace_size.argtypes = [i, i64, i64, i32, i32, i32]
+        L.dsc_attn_bwd_workspace_size.restype = sz
+        L.dsc_attn_bwd.argtypes = [p, i, i64, i64, i32, i32, i32, p, i64, p, i64, p, i64, p, p, p, p, i32, f32,
+                                   p, i64, p, i64, p, i64, p, sz]
+        L.dsc_kv_append.argtypes = [p, i, i64, i32, i32, i32, i32, p, i64, p, i64, p, i64, p, p, p, i64, p, p, i64,
+                                    i32, p, i64, p]
+        L.dsc_attn_decode_workspace_size.argtypes = [i, i64, i32, i32, i32, i32, i64]
+        L.dsc_attn_decode_workspace_size.restype = sz
+        L.dsc_attn_decode.argtypes = [p, i, i64, i32, i32, i32, p, i64, p, p, i64, i32, p, i64, p, f32, p, p, sz]
         L.dsc_bench_stream.argtypes = [p, p, i64, p, i64, i32, i32, i32, i32, i64]
         for f in ("dsc_bench_stream", "dsc_lowrank_bwd_noalloc", "dsc_headwise_fwd", "dsc_headwise_bwd", "dsc_lowrank_fwd", "dsc_lowrank_bwd",
                   "dsc_lowrank_bwd_deterministic", "dsc_static_bwd_deterministic",
@@ -76,7 +87,7 @@ def lib() -> ctypes.CDLL:
                   "dsc_state_from_prefill", "dsc_rope_table", "dsc_headwise_rope_fwd",
                   "dsc_headwise_rope_bwd", "dsc_headwise_rope_decode", "dsc_lowrank_rope_fwd",
                   "dsc_lowrank_rope_bwd", "dsc_headwise_gen_fwd", "dsc_headwise_gen_bwd", "dsc_generate_filters",
-                  "dsc_abi_version"):
+                  "dsc_attn_fwd", "dsc_attn_bwd", "dsc_kv_append", "dsc_attn_decode", "dsc_abi_version"):
             getattr(L, f).restype = ctypes.c_int
         L.dsc_status_string.argtypes = [i]
         L.dsc_status_string.restype = ctypes.c_char_p
@@ -360,6 +371,138 @@ def dsc_state_from_prefill(x, state, *, W, cu_seqlens=None, stream=None) -> None
     cu, ns = _seq(cu_seqlens)
     _check(lib().dsc_state_from_prefill(_stream(stream), _dtype_code(x), B, T, D, W, _ptr(x), cu, ns,
                                         _ptr(state)))
+
+
+def _rows(t: torch.Tensor, name: str):
+    """Pointer and row stride of token rows (..., heads, head_dim), a view of wider rows or dense."""
+    if t.stride(-1) != 1 or t.stride(-2) != t.shape[-1] and t.shape[-2] > 1:
+        raise ValueError(f"{name}: heads and channels must be contiguous within a token's row")
+    rs = t.stride(-3)
+    if t.shape[-3] == 1:  # a single row per leading index: rows are the leading stride apart
+        rs = t.stride(0) if t.dim() == 4 and t.shape[0] > 1 else t.shape[-2] * t.shape[-1]
+    elif t.dim() == 4 and t.shape[0] > 1 and t.stride(0) != t.shape[1] * rs:
+        raise ValueError(f"{name}: token rows must be evenly spaced")
+    return ctypes.c_void_p(t.data_ptr()), rs
+
+
+def _same(ref: torch.Tensor, **tensors):
+    """The tensors given have the type and device of ref."""
+    for name, t in tensors.items():
+        if t is not None and (t.dtype != ref.dtype or t.device != ref.device):
+            raise TypeError(f"{name} must be {ref.dtype} on {ref.device}")
+
+
+def _int32(ref: torch.Tensor, **tensors):
+    for name, t in tensors.items():
+        if t is not None and (t.dtype != torch.int32 or t.device != ref.device):
+            raise TypeError(f"{name} must be int32 on {ref.device}")
+
+
+def _attn_shapes(q, k, v):
+    if q.dim() != 4 or k.dim() != 4 or k.shape != v.shape or q.shape[:2] != k.shape[:2] or q.shape[3] != k.shape[3]:
+        raise ValueError("q must be (B,T,Hq,head_dim), k and v (B,T,Hkv,head_dim)")
+    _same(q, k=k, v=v)
+
+
+def _lse(lse, q):
+    B, T, Hq, _ = q.shape
+    if lse.dtype != torch.float32 or lse.shape != (Hq, B * T) or lse.device != q.device:
+        raise ValueError(f"lse must be fp32 ({Hq}, {B * T}) on {q.device}")
+    return _ptr(lse)
+
+
+def dsc_attn_fwd(q, k, v, o, lse=None, *, scale=None, cu_seqlens=None, stream=None) -> None:
+    """o (B,T,Hq,hd) <- causal attention of q (B,T,Hq,hd) over k, v (B,T,Hkv,hd), views of [Q | K | V] rows or
+    dense; lse (Hq, B*T) fp32 <- the rows' log-sum-exp (optional).  scale defaults to 1/sqrt(hd)."""
+    _attn_shapes(q, k, v)
+    _same(q, o=o)
+    if o.shape != q.shape:
+        raise ValueError("o must have q's shape")
+    B, T, Hq, hd = q.shape
+    (qp, qs), (kp, ks), (vp, vs) = _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
+    _int32(q, cu_seqlens=cu_seqlens)
+    cu, ns = _seq(cu_seqlens)
+    _check(lib().dsc_attn_fwd(_stream(stream), _dtype_code(q), B, T, Hq, k.shape[2], hd, qp, qs, kp, ks, vp, vs, cu,
+                              ns, hd ** -0.5 if scale is None else scale, _ptr(o), None if lse is None else _lse(lse, q)))
+
+
+def dsc_attn_bwd_workspace_size(dtype: torch.dtype, B: int, T: int, Hq: int, Hkv: int, head_dim: int) -> int:
+    code = DSC_BF16 if dtype == torch.bfloat16 else DSC_FP32
+    return int(lib().dsc_attn_bwd_workspace_size(code, B, T, Hq, Hkv, head_dim))
+
+
+def dsc_attn_bwd(q, k, v, o, lse, dout, dq, dk, dv, workspace=None, *, scale=None, cu_seqlens=None,
+                 stream=None) -> None:
+    """Gradients dq, dk, dv (like q, k, v; views of one tensor or dense) of dsc_attn_fwd for L = <dout, o>."""
+    _attn_shapes(q, k, v)
+    _same(q, o=o, dout=dout, dq=dq, dk=dk, dv=dv)
+    if o.shape != q.shape or dout.shape != q.shape or dq.shape != q.shape or dk.shape != k.shape or dv.shape != k.shape:
+        raise ValueError("o, dout and dq must have q's shape, dk and dv k's")
+    B, T, Hq, hd = q.shape
+    (qp, qs), (kp, ks), (vp, vs) = _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
+    (dqp, dqs), (dkp, dks), (dvp, dvs) = _rows(dq, "dq"), _rows(dk, "dk"), _rows(dv, "dv")
+    _int32(q, cu_seqlens=cu_seqlens)
+    cu, ns = _seq(cu_seqlens)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().dsc_attn_bwd(_stream(stream), _dtype_code(q), B, T, Hq, k.shape[2], hd, qp, qs, kp, ks, vp, vs,
+                              _ptr(o), _lse(lse, q), _ptr(dout), cu, ns, hd ** -0.5 if scale is None else scale,
+                              dqp, dqs, dkp, dks, dvp, dvs, _ptr(workspace), ws_bytes))
+
+
+def _cache_shapes(k_cache, v_cache, page_table, S, hd):
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.shape[3] != hd:
+        raise ValueError(f"k_cache and v_cache must be (num_pages, Hkv, page_size, {hd})")
+    if page_table.dim() != 2 or page_table.shape[0] != S:
+        raise ValueError(f"page_table must be ({S}, max_pages)")
+
+
+def dsc_kv_append(k, v, k_cache, v_cache, page_table, start, *, q=None, q_out=None, table=None, cu_seqlens=None,
+                  stream=None) -> None:
+    """k, v (N,Hkv,hd) of new tokens into the paged cache (num_pages,Hkv,page,hd) at positions start[s] + i, rotated
+    with table (None: as they are); q (N,Hq,hd) rotated likewise into q_out.  One token per sequence without
+    cu_seqlens, else the sequences' offsets among the N tokens."""
+    N, Hkv, hd = k.shape
+    S = start.numel()
+    _cache_shapes(k_cache, v_cache, page_table, S, hd)
+    _same(k, v=v, k_cache=k_cache, v_cache=v_cache, q=q, q_out=q_out)
+    _int32(k, page_table=page_table, start=start, cu_seqlens=cu_seqlens)
+    if v.shape != k.shape or k_cache.shape[1] != Hkv:
+        raise ValueError("k, v and the caches must agree in their heads")
+    if cu_seqlens is not None and cu_seqlens.numel() != S + 1:
+        raise ValueError("cu_seqlens must hold one offset more than start")
+    (kp, ks), (vp, vs) = _rows(k, "k"), _rows(v, "v")
+    Hq, qp, qs, qop = Hkv, None, 0, None
+    if q is not None:
+        if q_out is None or q_out.shape != q.shape or q.shape[0] != N or q.shape[2] != hd:
+            raise ValueError("q and q_out must be (N, Hq, head_dim)")
+        Hq, (qp, qs), qop = q.shape[1], _rows(q, "q"), _ptr(q_out)
+    tp, max_pos = _table(table, hd)
+    _check(lib().dsc_kv_append(_stream(stream), _dtype_code(k), N, S, Hq, Hkv, hd, qp, qs, kp, ks, vp, vs,
+                               _ptr(cu_seqlens), _ptr(start), tp, max_pos, _ptr(k_cache), _ptr(v_cache),
+                               k_cache.shape[0], k_cache.shape[2], _ptr(page_table), page_table.shape[1], qop))
+
+
+def dsc_attn_decode_workspace_size(dtype: torch.dtype, S: int, Hq: int, Hkv: int, head_dim: int, page_size: int,
+                                   max_pages: int) -> int:
+    code = DSC_BF16 if dtype == torch.bfloat16 else DSC_FP32
+    return int(lib().dsc_attn_decode_workspace_size(code, S, Hq, Hkv, head_dim, page_size, max_pages))
+
+
+def dsc_attn_decode(q, k_cache, v_cache, page_table, lens, o, workspace=None, *, scale=None, stream=None) -> None:
+    """o (S,Hq,hd) <- attention of one new token per sequence, q (S,Hq,hd), over the first lens[s] tokens of the
+    paged cache (num_pages,Hkv,page,hd).  scale defaults to 1/sqrt(hd)."""
+    S, Hq, hd = q.shape
+    _cache_shapes(k_cache, v_cache, page_table, S, hd)
+    _same(q, k_cache=k_cache, v_cache=v_cache, o=o)
+    _int32(q, page_table=page_table, lens=lens)
+    if o.shape != q.shape or lens.numel() != S:
+        raise ValueError("o must have q's shape, lens one length per sequence")
+    qp, qs = _rows(q, "q")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().dsc_attn_decode(_stream(stream), _dtype_code(q), S, Hq, k_cache.shape[1], hd, qp, qs, _ptr(k_cache),
+                                 _ptr(v_cache), k_cache.shape[0], k_cache.shape[2], _ptr(page_table),
+                                 page_table.shape[1], _ptr(lens), hd ** -0.5 if scale is None else scale, _ptr(o),
+                                 _ptr(workspace), ws_bytes))
 
 
 def dsc_bench_stream(src, read_bytes: int, dst, write_bytes: int, *, unroll=4, load_nt=False, store_nt=False,

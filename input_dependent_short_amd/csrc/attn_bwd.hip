@@ -1,0 +1,319 @@
+// attn_bwd.hip -- gradients of the causal attention of attn_fwd.hip, for
+// gfx950.  With g = dL/do, p_ij = exp(scale <q_i, k_j> - lse_i):
+//   delta_i = <g_i, o_i>,  ds_ij = scale * p_ij (<g_i, v_j> - delta_i),
+//   dq_i = sum_j ds_ij k_j,
+//   dk_j = sum_i ds_ij q_i,  dv_j = sum_i p_ij g_i   (over the group's heads).
+// Two kernels, no atomics, so every sum has one fixed order:
+//   attn_dq_kernel   block = 128 query rows of a head; walks the keys; also
+//                    forms delta and leaves it with log2(e) * lse in the
+//                    workspace for the second kernel;
+//   attn_dkv_kernel  block = 128 keys of a key head; walks the query rows of
+//                    every head of the group, so that the sum over the heads
+//                    stays in registers.
+// Forming the scores twice costs two of seven products; the alternative, one
+// walk with dq summed by atomics, would add each fp32 row of dq once per key
+// tile in an order that changes from run to run.
+#include "attn_common.h"
+
+namespace dsc {
+namespace {
+
+struct BwdParams {
+    const void *q, *k, *v, *o, *dout;
+    const float *lse;
+    void *dq, *dk, *dv;
+    float *delta, *lse2;  // workspace (Hq, N) each
+    SeqMap seq;
+    int64_t N, qs, ks, vs, dqs, dks, dvs;
+    int32_t Hq, Hkv, G, hd;
+    float scale, c2;
+    int64_t ntiles;
+};
+
+template <class E>
+constexpr int kBT = sizeof(typename E::store_t) == 2 ? 64 : 32;  // rows per walked tile
+
+template <class E, int HDC>
+__global__ __launch_bounds__(256, sizeof(typename E::store_t) == 2 ? 2 : 1) void attn_dq_kernel(BwdParams p) {
+    using T = Tile<E, HDC>;
+    using M = Mma<E>;
+    using S = typename E::store_t;
+    using frag = typename M::frag;
+    constexpr int BN = kBT<E>, BM = 128, NS = BN / 32, KF = HDC / M::KC, DT = HDC / 32, PF = 16 / M::PR;
+    __shared__ __align__(16) unsigned char k0s[BN * T::RB], v0s[BN * T::RB], k1s[BN * T::RB], v1s[BN * T::RB];
+    __shared__ int flag;
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
+    const int64_t lb = xcd_block_id(blockIdx.x, (int64_t)gridDim.x);
+    const int g = (int)(lb % p.G);
+    const int64_t rest = lb / p.G;
+    const int kvh = (int)(rest / p.ntiles);
+    const int64_t tile = p.ntiles - 1 - rest % p.ntiles;
+    const int qh = kvh * p.G + g;
+    const int64_t m0 = tile * BM, w0 = m0 + 32 * wave, row = w0 + (lane & 31);
+
+    int64_t start, blk_start, end;
+    p.seq.find((m0 + BM < p.N ? m0 + BM : p.N) - 1, start, end);
+    const int blk_last_start = (int)start;
+    p.seq.find(m0, blk_start, end);
+    if (tid == 0) flag = -1;
+    p.seq.find(row < p.N ? row : p.N - 1, start, end);
+    const int kv0 = (int)blk_start, kv_end = (int)min(m0 + BM, p.N);
+    const int wlast = (int)min(w0 + 31, p.N - 1);
+    const int wfirst_key = __builtin_amdgcn_readlane((int)start, 0);
+    const int wlast_start = __builtin_amdgcn_readlane((int)start, 31);
+    const int qi = (int)row, lo = (int)start;
+
+    const S *kb = static_cast<const S *>(p.k) + (int64_t)kvh * p.hd;
+    const S *vb = static_cast<const S *>(p.v) + (int64_t)kvh * p.hd;
+    auto issue = [&](int n0, unsigned char *ks, unsigned char *vs) __attribute__((always_inline)) {
+        if (n0 >= kv_end) return;
+        T::template load<BN, 4>(ks, kb, p.ks, n0, kv_end, p.hd, wave, lane);
+        T::template load<BN, 4>(vs, vb, p.vs, n0, kv_end, p.hd, wave, lane);
+    };
+
+    frag qf[KF], gf[KF];
+    const int64_t os = (int64_t)p.Hq * p.hd;
+    T::load_row(qf, static_cast<const S *>(p.q) + (int64_t)qh * p.hd, p.qs, row, p.N, p.hd, lane);
+    T::load_row(gf, static_cast<const S *>(p.dout) + (int64_t)qh * p.hd, os, row, p.N, p.hd, lane);
+    float delta = 0.f;
+    {
+        frag of[KF];
+        T::load_row(of, static_cast<const S *>(p.o) + (int64_t)qh * p.hd, os, row, p.N, p.hd, lane);
+#pragma unroll
+        for (int kc = 0; kc < KF; ++kc)
+#pragma unroll
+            for (int j = 0; j < T::VEC; ++j) delta = __builtin_fmaf((float)gf[kc][j], (float)of[kc][j], delta);
+    }
+    delta += other_half(delta);
+    const float lse2 = row < p.N ? p.lse[(int64_t)qh * p.N + row] * kLog2e : 0.f;
+    if (h == 0 && row < p.N) {
+        p.delta[(int64_t)qh * p.N + row] = delta;
+        p.lse2[(int64_t)qh * p.N + row] = lse2;
+    }
+
+    floatx16 acc[DT];
+#pragma unroll
+    for (int d = 0; d < DT; ++d) acc[d] = zero16();
+
+    auto compute = [&](int n0, bool dirty, const unsigned char *ks, const unsigned char *vs) __attribute__((always_inline)) {
+        if (n0 > wlast || n0 + BN <= wfirst_key) return;
+        const bool masked = n0 + BN - 1 > (int)w0 || n0 < wlast_start;
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+            floatx16 s = zero16(), dp = zero16();
+#pragma unroll
+            for (int kc = 0; kc < KF; ++kc) s = M::mul(T::read_row(ks, 32 * j, kc, lane), qf[kc], s);
+#pragma unroll
+            for (int kc = 0; kc < KF; ++kc) dp = M::mul(T::read_row(vs, 32 * j, kc, lane), gf[kc], dp);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], p.c2, -lse2)) * (dp[i] - delta);
+            if (masked) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int key = n0 + 32 * j + res_row(i, h);
+                    if (key > qi || key < lo) s[i] = 0.f;
+                }
+            }
+            // a key that is not finite leaves NaN in ds of the rows that see it, so no open pair is lost
+            if (__builtin_expect(dirty, 0)) {
+#pragma unroll
+                for (int f = 0; f < PF; ++f) {
+                    const frag df = M::pack(s, f);
+#pragma unroll
+                    for (int d = 0; d < DT; ++d)
+                        acc[d] = M::mul(T::finite(T::read_tr(ks, 32 * j, f, d, lane)), df, acc[d]);
+                }
+                continue;
+            }
+#pragma unroll
+            for (int f = 0; f < PF; ++f) {
+                const frag df = M::pack(s, f);
+#pragma unroll
+                for (int d = 0; d < DT; ++d) acc[d] = M::mul(T::read_tr(ks, 32 * j, f, d, lane), df, acc[d]);
+            }
+        }
+    };
+    auto step = [&](int n0, unsigned char *ks, unsigned char *vs, unsigned char *kn,
+                    unsigned char *vn) __attribute__((always_inline)) {
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        issue(n0 + BN, kn, vn);
+        const bool dirty = (n0 + BN - 1 > (int)m0 || n0 < blk_last_start) &&
+                           tile_dirty<T, BN, 4, false>(ks, nullptr, &flag, n0, wave, lane);
+        compute(n0, dirty, ks, vs);
+    };
+    issue(kv0, k0s, v0s);
+    for (int n0 = kv0; n0 < kv_end; n0 += 2 * BN) {
+        step(n0, k0s, v0s, k1s, v1s);
+        if (n0 + BN < kv_end) step(n0 + BN, k1s, v1s, k0s, v0s);
+    }
+    T::store_row(acc, p.scale, static_cast<S *>(p.dq) + (int64_t)qh * p.hd, p.dqs, row, p.N, p.hd, lane);
+}
+
+template <class E, int HDC>
+__global__ __launch_bounds__(256, sizeof(typename E::store_t) == 2 ? 2 : 1) void attn_dkv_kernel(BwdParams p) {
+    using T = Tile<E, HDC>;
+    using M = Mma<E>;
+    using S = typename E::store_t;
+    using frag = typename M::frag;
+    constexpr int BQ = kBT<E>, BK = 128, NS = BQ / 32, KF = HDC / M::KC, DT = HDC / 32, PF = 16 / M::PR;
+    __shared__ __align__(16) unsigned char q0s[BQ * T::RB], g0s[BQ * T::RB], q1s[BQ * T::RB], g1s[BQ * T::RB];
+    __shared__ int flag;
+    __shared__ __align__(16) float l0s[64], d0s[64], l1s[64], d1s[64];  // lse2, delta of the tile's rows
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
+    const int64_t lb = xcd_block_id(blockIdx.x, (int64_t)gridDim.x);
+    const int kvh = (int)(lb / p.ntiles);
+    const int64_t n0b = (lb % p.ntiles) * BK, w0 = n0b + 32 * wave, key = w0 + (lane & 31);
+
+    int64_t start, end, blk_end;
+    const int64_t blk_last = min(n0b + BK, p.N) - 1;
+    p.seq.find(n0b, start, end);
+    const int blk_first_end = (int)end;
+    p.seq.find(blk_last, start, blk_end);
+    if (tid == 0) flag = -1;
+    p.seq.find(key < p.N ? key : p.N - 1, start, end);
+    const int q_end = (int)blk_end, q0 = (int)n0b;
+    const int wfirst_end = __builtin_amdgcn_readlane((int)end, 0);   // rows below it see the wave's first key
+    const int wlast_end = __builtin_amdgcn_readlane((int)end, 31);   // rows at or past it see no key of the wave
+    const int ki = (int)key, hi = (int)end;
+
+    frag kf[KF], vf[KF];
+    T::load_row(kf, static_cast<const S *>(p.k) + (int64_t)kvh * p.hd, p.ks, key, p.N, p.hd, lane);
+    T::load_row(vf, static_cast<const S *>(p.v) + (int64_t)kvh * p.hd, p.vs, key, p.N, p.hd, lane);
+
+    floatx16 dk[DT], dv[DT];
+#pragma unroll
+    for (int d = 0; d < DT; ++d) dk[d] = zero16(), dv[d] = zero16();
+
+    const int nt = (q_end - q0 + BQ - 1) / BQ, total = nt * p.G;
+    const int64_t os = (int64_t)p.Hq * p.hd;
+    auto issue = [&](int it, unsigned char *qt, unsigned char *gt, float *lt, float *dt) __attribute__((always_inline)) {
+        if (it >= total) return;
+        const int gi = it / nt, m0 = q0 + (it - gi * nt) * BQ;
+        const int64_t qh = (int64_t)kvh * p.G + gi;
+        T::template load<BQ, 4>(qt, static_cast<const S *>(p.q) + qh * p.hd, p.qs, m0, q_end, p.hd, wave, lane);
+        T::template load<BQ, 4>(gt, static_cast<const S *>(p.dout) + qh * p.hd, os, m0, q_end, p.hd, wave, lane);
+        if (wave < 2) {
+            const float *src = (wave == 0 ? p.lse2 : p.delta) + qh * p.N + m0;
+            const __amdgpu_buffer_rsrc_t rs = make_stream(src, 4 * (int64_t)min(BQ, q_end - m0));
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (attn_lds_void *)(wave == 0 ? lt : dt), 4, 4u * lane, 0, 0, 0);
+        }
+    };
+    auto compute = [&](int it, const unsigned char *qt, const unsigned char *gt, const float *lt, const float *dt) __attribute__((always_inline)) {
+        const int m0 = q0 + (it % nt) * BQ;
+        if (m0 + BQ <= (int)w0 || m0 >= wlast_end) return;
+        const bool masked = m0 < (int)w0 + 31 || m0 + BQ > wfirst_end;
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+            floatx16 s = zero16(), dp = zero16();
+#pragma unroll
+            for (int kc = 0; kc < KF; ++kc) s = M::mul(T::read_row(qt, 32 * j, kc, lane), kf[kc], s);
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                const float4 l = *reinterpret_cast<const float4 *>(lt + 32 * j + res_row(i, h));
+                s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], p.c2, -l.x));
+                s[i + 1] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i + 1], p.c2, -l.y));
+                s[i + 2] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i + 2], p.c2, -l.z));
+                s[i + 3] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i + 3], p.c2, -l.w));
+            }
+            uint32_t open = 0xffffu;  // rows of this lane's elements that see its key
+            if (masked) {
+                open = 0;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int qr = m0 + 32 * j + res_row(i, h);
+                    if (qr >= ki && qr < hi) open |= 1u << i;
+                    else s[i] = 0.f;
+                }
+            }
+#pragma unroll
+            for (int f = 0; f < PF; ++f) {
+                const frag pf = M::pack(s, f);
+#pragma unroll
+                for (int d = 0; d < DT; ++d) dv[d] = M::mul(T::read_tr(gt, 32 * j, f, d, lane), pf, dv[d]);
+            }
+#pragma unroll
+            for (int kc = 0; kc < KF; ++kc) dp = M::mul(T::read_row(gt, 32 * j, kc, lane), vf[kc], dp);
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                const float4 dl = *reinterpret_cast<const float4 *>(dt + 32 * j + res_row(i, h));
+                s[i] *= dp[i] - dl.x;
+                s[i + 1] *= dp[i + 1] - dl.y;
+                s[i + 2] *= dp[i + 2] - dl.z;
+                s[i + 3] *= dp[i + 3] - dl.w;
+            }
+            if (masked) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (!((open >> i) & 1)) s[i] = 0.f;
+            }
+#pragma unroll
+            for (int f = 0; f < PF; ++f) {
+                const frag df = M::pack(s, f);
+#pragma unroll
+                for (int d = 0; d < DT; ++d) dk[d] = M::mul(T::read_tr(qt, 32 * j, f, d, lane), df, dk[d]);
+            }
+        }
+    };
+    // Rows of a tile with masked pairs that are not finite are left out of its
+    // products.  A key that sees such a row still gets NaN in dk, from the
+    // row's lse (q) or delta (dout); dv gets the row's values after the walk.
+    bool spoilt = false;
+    auto tile_masked = [&](int m0) { return m0 < (int)n0b + BK - 1 || m0 + BQ > blk_first_end; };
+    auto step = [&](int it, unsigned char *qt, unsigned char *gt, float *lt, float *dt, unsigned char *qn,
+                    unsigned char *gn, float *ln, float *dn) __attribute__((always_inline)) {
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        issue(it + 1, qn, gn, ln, dn);
+        const int m0 = q0 + (it % nt) * BQ;
+        if (tile_masked(m0) && tile_dirty<T, BQ, 4, true>(qt, gt, &flag, it, wave, lane)) spoilt = true;
+        compute(it, qt, gt, lt, dt);
+    };
+    issue(0, q0s, g0s, l0s, d0s);
+    for (int it = 0; it < total; it += 2) {
+        step(it, q0s, g0s, l0s, d0s, q1s, g1s, l1s, d1s);
+        if (it + 1 < total) step(it + 1, q1s, g1s, l1s, d1s, q0s, g0s, l0s, d0s);
+    }
+    T::store_row(dk, p.scale, static_cast<S *>(p.dk) + (int64_t)kvh * p.hd, p.dks, key, p.N, p.hd, lane);
+    S *dvb = static_cast<S *>(p.dv) + (int64_t)kvh * p.hd;
+    T::store_row(dv, 1.f, dvb, p.dvs, key, p.N, p.hd, lane);
+    if (__builtin_expect(spoilt, 0))
+        for (int gi = 0; gi < p.G; ++gi)
+            T::add_nonfinite(dvb, p.dvs, key, p.N, p.hd,
+                             static_cast<const S *>(p.dout) + ((int64_t)kvh * p.G + gi) * p.hd, os, q0, q_end, lane,
+                             [&](int r) { return r >= ki && r < hi && tile_masked(r - (r - q0) % BQ); });
+}
+
+template <class E, int HDC>
+void launch(const BwdParams &p, hipStream_t s) {
+    hipLaunchKernelGGL((attn_dq_kernel<E, HDC>), dim3((unsigned)(p.ntiles * p.Hq)), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((attn_dkv_kernel<E, HDC>), dim3((unsigned)(p.ntiles * p.Hkv)), dim3(256), 0, s, p);
+}
+
+template <class E>
+void dispatch(const BwdParams &p, hipStream_t s) {
+    if (p.hd <= 64) launch<E, 64>(p, s);
+    else if (p.hd <= 96) launch<E, 96>(p, s);
+    else launch<E, 128>(p, s);
+}
+
+}  // namespace
+
+size_t attn_bwd_workspace(int64_t N, int32_t Hq) { return 2 * sizeof(float) * (size_t)N * (size_t)Hq; }
+
+hipError_t attn_bwd(const AttnProblem &a, hipStream_t s) {
+    float *delta = static_cast<float *>(a.ws);
+    BwdParams p{a.q, a.k, a.v, a.o, a.dout, a.lse, a.dq, a.dk, a.dv, delta, delta + a.N * a.Hq,
+                SeqMap{a.cu, a.n_seqs, a.T}, a.N, a.qs, a.ks, a.vs, a.dqs, a.dks, a.dvs, a.Hq, a.Hkv,
+                a.Hq / a.Hkv, a.hd, a.scale, a.scale * kLog2e, (a.N + 127) / 128};
+    if (a.dtype == Dtype::BF16) dispatch<BF16>(p, s);
+    else dispatch<F32>(p, s);
+    return hipGetLastError();
+}
+
+}  // namespace dsc

@@ -1,0 +1,299 @@
+// attn_common.h -- tiles and matrix-core fragments of the attention kernels
+// (attn_fwd.hip, attn_bwd.hip), gfx950, wave64.  Internal to libdsc.so.
+//
+// Every product runs on 32 x 32 matrix instructions: bf16 operands with
+// v_mfma_f32_32x32x16_bf16, fp32 operands with v_mfma_f32_32x32x2_f32 (four
+// steps per fragment), fp32 sums in both.  With lane l, c = l % 32, h = l / 32:
+//   operand fragment  16 bytes of row (or column) c: 8 bf16 / 4 fp32 values,
+//                     the contraction places (h, j) of the instruction;
+//   result            element i (0..15) is row 8*(i/4) + 4*h + i%4, column c.
+// A contraction may run over its places in any order as long as both operands
+// use the same one.  So a result tile R[x][y] (x the 32 rows) is, with no move
+// between lanes, the right operand of a product contracted over x: fragment f
+// takes elements 8f..8f+7 (bf16) or 4f..4f+3 (fp32), which puts row
+// kRun*f*2 + 4h + (0..3) (and 8 further on for bf16) at the places of half h,
+// and the left operand is read from LDS at those same rows (read_tr).
+#pragma once
+
+#include "dsc_common.h"
+#include "dsc_kernels.h"
+
+namespace dsc {
+
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+typedef short shortx4 __attribute__((ext_vector_type(4)));
+typedef short shortx8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) void attn_lds_void;
+typedef __attribute__((address_space(3))) shortx4 attn_lds_s4;
+
+template <class E>
+struct Mma;
+
+template <>
+struct Mma<BF16> {
+    using frag = bf16x8;
+    static constexpr int KC = 16;  // contraction places per fragment
+    static constexpr int PR = 8;   // result elements per fragment
+    __device__ __forceinline__ static floatx16 mul(frag a, frag b, floatx16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+    }
+    // Elements PR*f .. of a result tile, rounded to nearest even: the matrix
+    // cores take bf16 operands (relative error 2^-9 per element, averaged by
+    // the sums over them).
+    __device__ __forceinline__ static frag pack(const floatx16 &r, int f) {
+        const uint4 q = make_uint4(pack_bf16x2(r[8 * f], r[8 * f + 1]), pack_bf16x2(r[8 * f + 2], r[8 * f + 3]),
+                                   pack_bf16x2(r[8 * f + 4], r[8 * f + 5]), pack_bf16x2(r[8 * f + 6], r[8 * f + 7]));
+        return __builtin_bit_cast(frag, q);
+    }
+};
+
+template <>
+struct Mma<F32> {
+    using frag = floatx4;
+    static constexpr int KC = 8;
+    static constexpr int PR = 4;
+    __device__ __forceinline__ static floatx16 mul(frag a, frag b, floatx16 c) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[s], b[s], c, 0, 0, 0);
+        return c;
+    }
+    __device__ __forceinline__ static frag pack(const floatx16 &r, int f) {
+        return frag{r[4 * f], r[4 * f + 1], r[4 * f + 2], r[4 * f + 3]};
+    }
+};
+
+__device__ __forceinline__ floatx16 zero16() {
+    floatx16 z;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) z[i] = 0.f;
+    return z;
+}
+
+// Row of result element i in half h.
+__device__ __forceinline__ constexpr int res_row(int i, int h) { return 8 * (i / 4) + 4 * h + i % 4; }
+
+// A tile of ROWS token rows in LDS, HDC channels of them used (a multiple of
+// 32, channels past the head's own are zero).  A row holds NCH 16-byte chunks
+// (a power of two), chunk c of row r at place c ^ swz(r): the rows that one
+// read_row touches (32 consecutive rows, one chunk) and the row quads that
+// one read_tr touches fall on distinct banks, whether the LDS serves 32 or
+// 64 banks per cycle.
+template <class E, int HDC>
+struct Tile {
+    using S = typename E::store_t;
+    using M = Mma<E>;
+    using frag = typename M::frag;
+    static constexpr int VEC = E::kVec;
+    static constexpr int RS = HDC <= 64 ? 64 : 128;  // channels per LDS row
+    static constexpr int NCH = RS / VEC;
+    static constexpr int RB = RS * (int)sizeof(S);   // bytes per row
+
+    __device__ __forceinline__ static int swz(int r) {
+        if constexpr (sizeof(S) == 4) return r & 7;
+        else if constexpr (RS == 64) return ((r & 2) << 1) | (((r ^ (r >> 3)) & 1) << 1) | ((r >> 2) & 1);
+        else return (r & 2) | ((r & 1) << 2) | ((r >> 2) & 1) | (((r << 2) ^ r) & 8);
+    }
+
+    // Rows row0 .. row0+ROWS-1 of a (N, stride) tensor's head (base: its first
+    // channel, hd channels) straight from memory into the LDS tile, by the
+    // block's NW waves.  Rows at or past N and channels at or past hd read as
+    // zero (past the buffer resource).
+    template <int ROWS, int NW>
+    __device__ __forceinline__ static void load(unsigned char *lds, const S *base, int64_t stride, int64_t row0,
+                                                int64_t N, int hd, int wave, int lane) {
+        constexpr int INST = ROWS * RB / 1024;
+        static_assert(INST % NW == 0, "tile split");
+        int64_t left = N - row0;
+        left = left < 0 ? 0 : (left > ROWS ? ROWS : left);
+        const __amdgpu_buffer_rsrc_t rs =
+            make_stream(base + row0 * stride, left > 0 ? ((left - 1) * stride + hd) * (int64_t)sizeof(S) : 0);
+#pragma unroll
+        for (int j = 0; j < INST / NW; ++j) {
+            const int i = j * NW + wave;
+            const int slot = 64 * i + lane;
+            const int row = slot / NCH, c = (slot % NCH) ^ swz(row);
+            const uint32_t off = (uint32_t)row * (uint32_t)(stride * sizeof(S)) + 16u * c;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (attn_lds_void *)(lds + 1024 * i), 16,
+                                                     VEC * c < hd ? off : kFar, 0, 0, 0);
+        }
+    }
+
+    // Fragment kc of row r0 + lane%32: channels KC*kc ...
+    __device__ __forceinline__ static frag read_row(const unsigned char *lds, int r0, int kc, int lane) {
+        const int r = r0 + (lane & 31);
+        return *reinterpret_cast<const frag *>(lds + r * RB + 16 * ((2 * kc + (lane >> 5)) ^ swz(r)));
+    }
+
+    // Fragment of the transposed tile: channel 32*dt + lane%32, the rows of
+    // result fragment f counted from r0 (a multiple of 16).
+    __device__ __forceinline__ static frag read_tr(const unsigned char *lds, int r0, int f, int dt, int lane) {
+        if constexpr (sizeof(S) == 2) {
+            // a 16-lane group reads a 4 x 16 block, lane i its 8-byte piece i, and gets column i
+            const int i = lane & 15, r = r0 + 16 * f + 4 * (lane >> 5) + (i >> 2);
+            const int c = 4 * dt + ((lane >> 3) & 2) + ((i >> 1) & 1);
+            const unsigned char *p0 = lds + r * RB + 16 * (c ^ swz(r)) + 8 * (i & 1);
+            const unsigned char *p1 = lds + (r + 8) * RB + 16 * (c ^ swz(r + 8)) + 8 * (i & 1);
+            const shortx4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((attn_lds_s4 *)p0);
+            const shortx4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((attn_lds_s4 *)p1);
+            return __builtin_bit_cast(frag, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+        } else {
+            const int d = 32 * dt + (lane & 31);
+            frag v;
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const int r = r0 + 8 * f + 4 * (lane >> 5) + s;
+                v[s] = *reinterpret_cast<const float *>(lds + r * RB + 16 * ((d >> 2) ^ swz(r)) + 4 * (d & 3));
+            }
+            return v;
+        }
+    }
+
+    // The same fragment with zeros for its non-finite values.
+    __device__ __forceinline__ static frag finite(frag v) {
+        const uint4 u = __builtin_bit_cast(uint4, v);
+        uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(S) == 4) {
+                if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] = 0;
+            } else {
+                if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u;
+                if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0xffffu;
+            }
+        }
+        return __builtin_bit_cast(frag, make_uint4(w[0], w[1], w[2], w[3]));
+    }
+
+    // Whether this wave's part (one in NW) of a tile of ROWS rows holds a
+    // value that is not finite: the largest magnitude, as an integer.
+    template <int ROWS, int NW>
+    __device__ __forceinline__ static bool scan(const unsigned char *lds, int wave, int lane) {
+        typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+        constexpr int PER = ROWS * RB / 1024 / NW;
+        u16x2 m2 = {0, 0};
+        uint32_t m1 = 0;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(lds + 1024 * (j * NW + wave) + 16 * lane);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (sizeof(S) == 4) m1 = max(m1, w[i] & 0x7fffffffu);
+                else m2 = __builtin_elementwise_max(m2, __builtin_bit_cast(u16x2, w[i] & 0x7fff7fffu));
+            }
+        }
+        const bool bad = sizeof(S) == 4 ? m1 >= 0x7f800000u : (m2[0] >= 0x7f80 || m2[1] >= 0x7f80);
+        return __any(bad);
+    }
+
+    // This wave's part of the tile with zeros for its non-finite values, in place.
+    template <int ROWS, int NW>
+    __device__ __forceinline__ static void clean(unsigned char *lds, int wave, int lane) {
+#pragma unroll
+        for (int j = 0; j < ROWS * RB / 1024 / NW; ++j) {
+            frag *p = reinterpret_cast<frag *>(lds + 1024 * (j * NW + wave) + 16 * lane);
+            *p = finite(*p);
+        }
+    }
+
+    // dst[row][d] += X[r][d] for the non-finite values X of the token rows r in
+    // [r0, r1) of a (N, stride) tensor that open(r) admits for this lane's row,
+    // over the channels that store_row gave this lane.
+    template <class Open>
+    __device__ __forceinline__ static void add_nonfinite(S *dst, int64_t dstride, int64_t row, int64_t N, int hd,
+                                                         const S *src, int64_t stride, int r0, int r1, int lane,
+                                                         const Open &open) {
+        if (row >= N) return;
+#pragma clang loop unroll(disable)
+        for (int d = 4 * (lane >> 5); d < hd; d += 8) {
+            S *o = dst + row * dstride + d;
+            float a[4] = {0.f, 0.f, 0.f, 0.f};
+            bool any = false;
+#pragma clang loop unroll(disable)
+            for (int r = r0; r < r1; ++r) {
+                if (!open(r)) continue;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float x = load_elem<E>(src + r * stride + d + i);
+                    if ((__float_as_uint(x) & 0x7f800000u) == 0x7f800000u) a[i] += x, any = true;
+                }
+            }
+            if (!any) continue;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float v = load_elem<E>(o + i) + a[i];
+                if constexpr (sizeof(S) == 4) o[i] = v;
+                else o[i] = to_bf16(v);
+            }
+        }
+    }
+
+    // Fragments of one token row (lane%32's) straight from memory; zero
+    // outside the tensor and past the head.
+    __device__ __forceinline__ static void load_row(frag (&f)[HDC / M::KC], const S *base, int64_t stride, int64_t row,
+                                                    int64_t N, int hd, int lane) {
+#pragma unroll
+        for (int kc = 0; kc < HDC / M::KC; ++kc) {
+            const int d = VEC * (2 * kc + (lane >> 5));
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (row < N && d < hd) v = *reinterpret_cast<const uint4 *>(base + row * stride + d);
+            f[kc] = __builtin_bit_cast(frag, v);
+        }
+    }
+
+    // A transposed result (channel 32*dt + res_row(i, h), token row lane%32)
+    // to the token's row in memory, four channels at a time.
+    __device__ __forceinline__ static void store_row(const floatx16 (&r)[HDC / 32], float mul, S *base, int64_t stride,
+                                                     int64_t row, int64_t N, int hd, int lane) {
+        if (row >= N) return;
+        S *p = base + row * stride + 4 * (lane >> 5);
+#pragma unroll
+        for (int dt = 0; dt < HDC / 32; ++dt)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int d = 32 * dt + 8 * q;
+                if (d + 4 * (lane >> 5) >= hd) continue;
+                const float a = r[dt][4 * q] * mul, b = r[dt][4 * q + 1] * mul, c = r[dt][4 * q + 2] * mul,
+                            e = r[dt][4 * q + 3] * mul;
+                if constexpr (sizeof(S) == 4)
+                    *reinterpret_cast<float4 *>(p + d) = make_float4(a, b, c, e);
+                else
+                    *reinterpret_cast<uint2 *>(p + d) = make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, e));
+            }
+    }
+};
+
+// The other half's value (lane ^ 32).
+__device__ __forceinline__ float other_half(float v) {
+    const uint32_t u = __float_as_uint(v);
+    const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
+}
+
+// A masked pair has probability zero, but zero times a non-finite value is
+// NaN inside a product.  So where a tile has masked pairs (the diagonal, a
+// sequence boundary) its rows are scanned, and non-finite values are kept out
+// of the product: a row's result never depends on tokens it must not see.
+// tile_dirty tells whether the tile a (and b) of ROWS rows holds one; every
+// wave of the block calls it for the same tiles; `tag` differs from tile to
+// tile, *flag is an LDS word that holds no tag at first.  With CLEAN they are
+// zeroed in place, and the caller gives the open pairs theirs by other means.
+template <class T, int ROWS, int NW, bool CLEAN>
+__device__ __forceinline__ bool tile_dirty(unsigned char *a, unsigned char *b, int *flag, int tag, int wave, int lane) {
+    bool bad = T::template scan<ROWS, NW>(a, wave, lane);
+    if (b) bad |= T::template scan<ROWS, NW>(b, wave, lane);
+    if (bad) *flag = tag;
+    lds_barrier();
+    const bool dirty = __builtin_amdgcn_readfirstlane(*flag) == tag;
+    if (CLEAN && __builtin_expect(dirty, 0)) {
+        T::template clean<ROWS, NW>(a, wave, lane);
+        if (b) T::template clean<ROWS, NW>(b, wave, lane);
+        lds_barrier();
+    }
+    return dirty;
+}
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+}  // namespace dsc

@@ -1,0 +1,187 @@
+// attn_fwd.hip -- causal attention over whole prompts, grouped heads, packed
+// sequences, for gfx950:
+//   s_ij = scale * <q_i, k_j>  for j <= i in i's sequence,
+//   o_i  = sum_j p_ij v_j,  p_ij = exp(s_ij - lse_i),  lse_i = log sum_j exp(s_ij).
+// One pass over the keys with the running maximum and sum of each row.
+//
+// Block = 128 query rows of one query head, on the flattened token axis (a
+// tile may hold parts of several sequences), 32 rows per wave.  The keys run
+// from the first token of the first row's sequence to the last row, kBN at a
+// time, K and V tiles loaded straight into two alternating LDS stages.
+// Scores are formed transposed (S^T = K Q^T), so a lane holds 16 keys of one
+// query row per 32 x 32 tile: row statistics need one exchange between the
+// wave's halves, and the probabilities are the right operand of O^T = V^T P^T
+// without moving between lanes.
+#include "attn_common.h"
+
+namespace dsc {
+namespace {
+
+struct FwdParams {
+    const void *q, *k, *v;
+    void *o;
+    float *lse;
+    SeqMap seq;
+    int64_t N, qs, ks, vs;
+    int32_t Hq, Hkv, G, hd;
+    float c2;  // scale * log2(e)
+    int64_t ntiles;
+};
+
+template <class E>
+constexpr int kBN = sizeof(typename E::store_t) == 2 ? 64 : 32;  // keys per tile
+
+template <class E, int HDC>
+__global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdParams p) {
+    using T = Tile<E, HDC>;
+    using M = Mma<E>;
+    using S = typename E::store_t;
+    using frag = typename M::frag;
+    constexpr int BN = kBN<E>, BM = 128, NS = BN / 32, KF = HDC / M::KC, DT = HDC / 32, PF = 16 / M::PR;
+    __shared__ __align__(16) unsigned char k0s[BN * T::RB], v0s[BN * T::RB], k1s[BN * T::RB], v1s[BN * T::RB];
+    __shared__ int flag;
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
+    const int64_t lb = xcd_block_id(blockIdx.x, (int64_t)gridDim.x);
+    const int g = (int)(lb % p.G);
+    const int64_t rest = lb / p.G;
+    const int kvh = (int)(rest / p.ntiles);
+    const int64_t tile = p.ntiles - 1 - rest % p.ntiles;
+    const int qh = kvh * p.G + g;
+    const int64_t m0 = tile * BM, w0 = m0 + 32 * wave, row = w0 + (lane & 31);
+
+    // sequence starts: the block's first row, this lane's row, the wave's last row
+    int64_t start, blk_start, end;
+    p.seq.find((m0 + BM < p.N ? m0 + BM : p.N) - 1, start, end);
+    const int blk_last_start = (int)start;
+    p.seq.find(m0, blk_start, end);
+    if (tid == 0) flag = -1;
+    p.seq.find(row < p.N ? row : p.N - 1, start, end);
+    const int kv0 = (int)blk_start;
+    const int kv_end = (int)min(m0 + BM, p.N);
+    const int wlast = (int)min(w0 + 31, p.N - 1);
+    const int wfirst_key = __builtin_amdgcn_readlane((int)start, 0);   // the wave needs keys from here
+    const int wlast_start = __builtin_amdgcn_readlane((int)start, 31); // every row is open from here
+    const int qi = (int)row, lo = (int)start;
+
+    const S *kb = static_cast<const S *>(p.k) + (int64_t)kvh * p.hd;
+    const S *vb = static_cast<const S *>(p.v) + (int64_t)kvh * p.hd;
+    frag qf[KF];
+    T::load_row(qf, static_cast<const S *>(p.q) + (int64_t)qh * p.hd, p.qs, row, p.N, p.hd, lane);
+
+    floatx16 acc[DT];
+#pragma unroll
+    for (int d = 0; d < DT; ++d) acc[d] = zero16();
+    float mx = -INFINITY, sum = 0.f;  // running maximum (both halves) of the raw scores, this half's sum
+
+    auto issue = [&](int n0, unsigned char *ks, unsigned char *vs) __attribute__((always_inline)) {
+        if (n0 >= kv_end) return;
+        T::template load<BN, 4>(ks, kb, p.ks, n0, kv_end, p.hd, wave, lane);
+        T::template load<BN, 4>(vs, vb, p.vs, n0, kv_end, p.hd, wave, lane);
+    };
+    auto compute = [&](int n0, const unsigned char *ks, const unsigned char *vs) __attribute__((always_inline)) {
+        if (n0 > wlast || n0 + BN <= wfirst_key) return;
+        floatx16 s[NS];
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+            s[j] = zero16();
+#pragma unroll
+            for (int kc = 0; kc < KF; ++kc) s[j] = M::mul(T::read_row(ks, 32 * j, kc, lane), qf[kc], s[j]);
+        }
+        if (n0 + BN - 1 > (int)w0 || n0 < wlast_start) {  // some pair of the tile is masked
+#pragma unroll
+            for (int j = 0; j < NS; ++j)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int key = n0 + 32 * j + res_row(i, h);
+                    if (key > qi || key < lo) s[j][i] = -INFINITY;
+                }
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int j = 0; j < NS; ++j)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, s[j][i]);
+        top = fmaxf(top, other_half(top));
+        if (__any(top > mx)) {
+            const float nm = fmaxf(mx, top);
+            const float safe = nm == -INFINITY ? 0.f : nm;
+            const float al = __builtin_amdgcn_exp2f((mx - safe) * p.c2);
+            mx = nm;
+            sum *= al;
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[d][i] *= al;
+        }
+        const float mc = mx == -INFINITY ? 0.f : mx * p.c2;
+#pragma unroll
+        for (int j = 0; j < NS; ++j)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                s[j][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j][i], p.c2, -mc));
+                sum += s[j][i];
+            }
+#pragma unroll
+        for (int j = 0; j < NS; ++j)
+#pragma unroll
+            for (int f = 0; f < PF; ++f) {
+                const frag pf = M::pack(s[j], f);
+#pragma unroll
+                for (int d = 0; d < DT; ++d) acc[d] = M::mul(T::read_tr(vs, 32 * j, f, d, lane), pf, acc[d]);
+            }
+    };
+    bool spoilt = false;  // V rows of a tile with masked pairs held non-finite values, left out of the product
+    auto masked = [&](int n0) { return n0 + BN - 1 > (int)m0 || n0 < blk_last_start; };
+    // A tile's loads are waited for, then a barrier shows them to every wave
+    // and ends every wave's reads of the other stage, which is refilled.
+    auto step = [&](int n0, unsigned char *ks, unsigned char *vs, unsigned char *kn,
+                    unsigned char *vn) __attribute__((always_inline)) {
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        issue(n0 + BN, kn, vn);
+        if (masked(n0) && tile_dirty<T, BN, 4, true>(vs, nullptr, &flag, n0, wave, lane)) spoilt = true;
+        compute(n0, ks, vs);
+    };
+    issue(kv0, k0s, v0s);
+    for (int n0 = kv0; n0 < kv_end; n0 += 2 * BN) {
+        step(n0, k0s, v0s, k1s, v1s);
+        if (n0 + BN < kv_end) step(n0 + BN, k1s, v1s, k0s, v0s);
+    }
+
+    sum += other_half(sum);
+    const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);  // NaN stays
+    S *ob = static_cast<S *>(p.o) + (int64_t)qh * p.hd;
+    T::store_row(acc, inv, ob, (int64_t)p.Hq * p.hd, row, p.N, p.hd, lane);
+    if (__builtin_expect(spoilt, 0))
+        T::add_nonfinite(ob, (int64_t)p.Hq * p.hd, row, p.N, p.hd, vb, p.vs, kv0, kv_end, lane, [&](int r) {
+            return r <= qi && r >= lo && masked(r - (r - kv0) % BN);
+        });
+    if (p.lse && h == 0 && row < p.N) p.lse[(int64_t)qh * p.N + row] = mx * p.c2 * kLn2 + __logf(sum);
+}
+
+template <class E, int HDC>
+void launch(const FwdParams &p, hipStream_t s) {
+    const int64_t blocks = p.ntiles * p.Hq;
+    hipLaunchKernelGGL((attn_fwd_kernel<E, HDC>), dim3((unsigned)blocks), dim3(256), 0, s, p);
+}
+
+template <class E>
+void dispatch(const FwdParams &p, hipStream_t s) {
+    if (p.hd <= 64) launch<E, 64>(p, s);
+    else if (p.hd <= 96) launch<E, 96>(p, s);
+    else launch<E, 128>(p, s);
+}
+
+}  // namespace
+
+hipError_t attn_fwd(const AttnProblem &a, hipStream_t s) {
+    FwdParams p{a.q, a.k, a.v, a.o, a.lse, SeqMap{a.cu, a.n_seqs, a.T}, a.N, a.qs, a.ks, a.vs, a.Hq, a.Hkv,
+                a.Hq / a.Hkv, a.hd, a.scale * kLog2e, (a.N + 127) / 128};
+    if (a.dtype == Dtype::BF16) dispatch<BF16>(p, s);
+    else dispatch<F32>(p, s);
+    return hipGetLastError();
+}
+
+}  // namespace dsc

@@ -659,6 +659,270 @@ dsc_status dsc_state_from_prefill(void *stream, int dtype, int64_t B, int64_t T,
                     "dsc_state_from_prefill launch");
 }
 
+// ------------------------------------------------ attention and its cache
+
+namespace {
+
+constexpr int64_t kMaxStride = (int64_t)1 << 20;  // elements between token rows: a tile's byte offsets stay in 32 bits
+constexpr int32_t kMaxHeadDim = 128;
+
+dsc_status check_heads(int dtype, int32_t Hq, int32_t Hkv, int32_t hd) {
+    if (dtype != DSC_FP32 && dtype != DSC_BF16) return fail(DSC_ERR_UNSUPPORTED, "unknown dtype %d", dtype);
+    if (Hkv < 1 || Hq < 1 || Hq % Hkv || Hq > (1 << 16))
+        return fail(DSC_ERR_SHAPE, "Hq = %d must be a multiple of Hkv = %d, both in 1..65536", Hq, Hkv);
+    const int vec = dtype == DSC_BF16 ? 8 : 4;
+    if (hd < 1) return fail(DSC_ERR_SHAPE, "head_dim = %d must be positive", hd);
+    if (hd % vec || hd > kMaxHeadDim)
+        return fail(DSC_ERR_UNSUPPORTED, "head_dim = %d must be a multiple of %d, at most %d", hd, vec, kMaxHeadDim);
+    return DSC_SUCCESS;
+}
+
+dsc_status check_scale(float scale) {
+    if (!(scale > 0.f) || scale > 3.0e38f) return fail(DSC_ERR_SHAPE, "scale must be positive and finite");
+    return DSC_SUCCESS;
+}
+
+// Rows of `heads` heads, `stride` elements apart.
+dsc_status check_stride(const char *name, int dtype, int64_t stride, int32_t heads, int32_t hd) {
+    const int vec = dtype == DSC_BF16 ? 8 : 4;
+    if (stride < (int64_t)heads * hd || stride > kMaxStride || stride % vec)
+        return fail(DSC_ERR_SHAPE, "%s_stride = %lld must be a multiple of %d in %lld..2^20", name, (long long)stride, vec,
+                    (long long)heads * hd);
+    return DSC_SUCCESS;
+}
+
+// A tensor of N token rows, `stride` bytes apart, `width` bytes of each.
+struct Rows {
+    const char *name;
+    uintptr_t p;
+    size_t n, stride, width;
+};
+
+Rows rows(const char *name, const void *p, size_t n, int64_t stride, int64_t width, size_t es) {
+    return Rows{name, (uintptr_t)p, n, (size_t)stride * es, (size_t)width * es};
+}
+
+// Whether two tensors share a byte.  Views of one wider row (equal strides)
+// may interleave: they are apart when their column ranges are.
+bool rows_meet(const Rows &a, const Rows &b) {
+    if (!a.n || !b.n || !a.p || !b.p) return false;
+    if (a.p + (a.n - 1) * a.stride + a.width <= b.p || b.p + (b.n - 1) * b.stride + b.width <= a.p) return false;
+    if (a.stride != b.stride) return true;
+    const size_t d = a.p <= b.p ? (b.p - a.p) % a.stride : (a.stride - (a.p - b.p) % a.stride) % a.stride;
+    return d < a.width || d + b.width > a.stride;
+}
+
+dsc_status check_rows(const Rows *in, int nin, const Rows *out, int nout) {
+    for (int i = 0; i < nout; ++i) {
+        for (int j = 0; j < nin; ++j)
+            if (rows_meet(out[i], in[j]))
+                return fail(DSC_ERR_ALIAS, "output %s overlaps input %s", out[i].name, in[j].name);
+        for (int j = i + 1; j < nout; ++j)
+            if (rows_meet(out[i], out[j])) return fail(DSC_ERR_ALIAS, "outputs %s and %s overlap", out[i].name, out[j].name);
+    }
+    return DSC_SUCCESS;
+}
+
+Rows flat(const char *name, const void *p, size_t bytes) { return Rows{name, (uintptr_t)p, bytes ? 1u : 0u, bytes, bytes}; }
+
+// Sizes shared by the whole-prompt calls.
+dsc_status check_attn(int dtype, int64_t B, int64_t T, int32_t Hq, int32_t Hkv, int32_t hd, const int32_t *cu,
+                      int32_t n_seqs) {
+    DSC_TRY(check_heads(dtype, Hq, Hkv, hd));
+    // the common checks of tokens and offsets; D stands for a row of the output, W and residual do not apply
+    DSC_TRY(check_common(dtype, B, T, (int64_t)Hq * hd, 1, cu, n_seqs, 0));
+    if (B * T > INT32_MAX - 512) return fail(DSC_ERR_SHAPE, "B*T = %lld tokens: too many", (long long)(B * T));
+    if (((B * T + 127) / 128) > INT32_MAX / Hq) return fail(DSC_ERR_SHAPE, "B*T * Hq too large");
+    return DSC_SUCCESS;
+}
+
+}  // namespace
+
+dsc_status dsc_attn_fwd(void *stream, int dtype, int64_t B, int64_t T, int32_t Hq, int32_t Hkv, int32_t head_dim,
+                        const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                        int64_t v_stride, const int32_t *cu_seqlens, int32_t n_seqs, float scale, void *o, float *lse) {
+    DSC_TRY(check_attn(dtype, B, T, Hq, Hkv, head_dim, cu_seqlens, n_seqs));
+    DSC_TRY(check_scale(scale));
+    DSC_TRY(check_stride("q", dtype, q_stride, Hq, head_dim));
+    DSC_TRY(check_stride("k", dtype, k_stride, Hkv, head_dim));
+    DSC_TRY(check_stride("v", dtype, v_stride, Hkv, head_dim));
+    if (B * T == 0) return ok();
+    if (!q || !k || !v || !o) return fail(DSC_ERR_NULL, "q, k, v and o are required");
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse))
+        return fail(DSC_ERR_ALIGNMENT, "pointers must be 16-byte aligned");
+    const size_t es = esize(dtype), N = (size_t)(B * T);
+    const int64_t qw = (int64_t)Hq * head_dim, kw = (int64_t)Hkv * head_dim;
+    const Rows in[] = {rows("q", q, N, q_stride, qw, es), rows("k", k, N, k_stride, kw, es),
+                       rows("v", v, N, v_stride, kw, es),
+                       flat("cu_seqlens", cu_seqlens, cu_seqlens ? 4u * ((size_t)n_seqs + 1) : 0)};
+    const Rows out[] = {rows("o", o, N, qw, qw, es), flat("lse", lse, lse ? N * Hq * 4u : 0)};
+    DSC_TRY(check_rows(in, 4, out, 2));
+    dsc::AttnProblem p{};
+    p.dtype = dtype == DSC_BF16 ? dsc::Dtype::BF16 : dsc::Dtype::F32;
+    p.N = B * T, p.T = T, p.Hq = Hq, p.Hkv = Hkv, p.hd = head_dim;
+    p.q = q, p.k = k, p.v = v, p.qs = q_stride, p.ks = k_stride, p.vs = v_stride;
+    p.cu = cu_seqlens, p.n_seqs = n_seqs, p.scale = scale, p.o = o, p.lse = lse;
+    return launched(dsc::attn_fwd(p, (hipStream_t)stream), "dsc_attn_fwd launch");
+}
+
+size_t dsc_attn_bwd_workspace_size(int dtype, int64_t B, int64_t T, int32_t Hq, int32_t Hkv, int32_t head_dim) {
+    if (check_attn(dtype, B, T, Hq, Hkv, head_dim, nullptr, 0) != DSC_SUCCESS) return 0;
+    return dsc::attn_bwd_workspace(B * T, Hq);
+}
+
+dsc_status dsc_attn_bwd(void *stream, int dtype, int64_t B, int64_t T, int32_t Hq, int32_t Hkv, int32_t head_dim,
+                        const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                        int64_t v_stride, const void *o, const float *lse, const void *dout,
+                        const int32_t *cu_seqlens, int32_t n_seqs, float scale, void *dq, int64_t dq_stride, void *dk,
+                        int64_t dk_stride, void *dv, int64_t dv_stride, void *workspace, size_t workspace_bytes) {
+    DSC_TRY(check_attn(dtype, B, T, Hq, Hkv, head_dim, cu_seqlens, n_seqs));
+    DSC_TRY(check_scale(scale));
+    DSC_TRY(check_stride("q", dtype, q_stride, Hq, head_dim));
+    DSC_TRY(check_stride("k", dtype, k_stride, Hkv, head_dim));
+    DSC_TRY(check_stride("v", dtype, v_stride, Hkv, head_dim));
+    DSC_TRY(check_stride("dq", dtype, dq_stride, Hq, head_dim));
+    DSC_TRY(check_stride("dk", dtype, dk_stride, Hkv, head_dim));
+    DSC_TRY(check_stride("dv", dtype, dv_stride, Hkv, head_dim));
+    if (B * T == 0) return ok();
+    if (!q || !k || !v || !o || !lse || !dout || !dq || !dk || !dv)
+        return fail(DSC_ERR_NULL, "q, k, v, o, lse, dout, dq, dk and dv are required");
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse) || !aligned16(dout) ||
+        !aligned16(dq) || !aligned16(dk) || !aligned16(dv) || !aligned16(workspace))
+        return fail(DSC_ERR_ALIGNMENT, "pointers must be 16-byte aligned");
+    const size_t need = dsc::attn_bwd_workspace(B * T, Hq);
+    if (!workspace || workspace_bytes < need)
+        return fail(DSC_ERR_WORKSPACE, "workspace of %zu bytes required (got %zu)", need, workspace ? workspace_bytes : 0);
+    const size_t es = esize(dtype), N = (size_t)(B * T);
+    const int64_t qw = (int64_t)Hq * head_dim, kw = (int64_t)Hkv * head_dim;
+    const Rows in[] = {rows("q", q, N, q_stride, qw, es), rows("k", k, N, k_stride, kw, es),
+                       rows("v", v, N, v_stride, kw, es), rows("o", o, N, qw, qw, es),
+                       rows("dout", dout, N, qw, qw, es), flat("lse", lse, N * Hq * 4u),
+                       flat("cu_seqlens", cu_seqlens, cu_seqlens ? 4u * ((size_t)n_seqs + 1) : 0)};
+    const Rows out[] = {rows("dq", dq, N, dq_stride, qw, es), rows("dk", dk, N, dk_stride, kw, es),
+                        rows("dv", dv, N, dv_stride, kw, es), flat("workspace", workspace, need)};
+    DSC_TRY(check_rows(in, 7, out, 4));
+    dsc::AttnProblem p{};
+    p.dtype = dtype == DSC_BF16 ? dsc::Dtype::BF16 : dsc::Dtype::F32;
+    p.N = B * T, p.T = T, p.Hq = Hq, p.Hkv = Hkv, p.hd = head_dim;
+    p.q = q, p.k = k, p.v = v, p.qs = q_stride, p.ks = k_stride, p.vs = v_stride;
+    p.cu = cu_seqlens, p.n_seqs = n_seqs, p.scale = scale;
+    p.o = const_cast<void *>(o), p.lse = const_cast<float *>(lse), p.dout = dout;
+    p.dq = dq, p.dk = dk, p.dv = dv, p.dqs = dq_stride, p.dks = dk_stride, p.dvs = dv_stride, p.ws = workspace;
+    return launched(dsc::attn_bwd(p, (hipStream_t)stream), "dsc_attn_bwd launch");
+}
+
+namespace {
+
+// The cache's sizes, shared by the two calls on it.
+dsc_status check_cache(int64_t S, int32_t Hkv, int32_t hd, int64_t num_pages, int32_t page_size, int64_t max_pages) {
+    if (S < 0 || S > INT32_MAX) return fail(DSC_ERR_SHAPE, "%lld sequences", (long long)S);
+    if (page_size < 1 || page_size > (1 << 20)) return fail(DSC_ERR_SHAPE, "page_size = %d must be in 1..2^20", page_size);
+    if (num_pages < 0 || num_pages > INT32_MAX) return fail(DSC_ERR_SHAPE, "num_pages = %lld out of range", (long long)num_pages);
+    if (max_pages < 1 || max_pages > (int64_t)(1 << 30) / page_size)
+        return fail(DSC_ERR_SHAPE, "max_pages = %lld: 1 <= max_pages * page_size <= 2^30 required", (long long)max_pages);
+    if (S > 0 && max_pages > ((int64_t)1 << 40) / S) return fail(DSC_ERR_SHAPE, "page table too large");
+    if (num_pages > ((int64_t)1 << 46) / ((int64_t)page_size * Hkv * hd)) return fail(DSC_ERR_SHAPE, "cache too large");
+    return DSC_SUCCESS;
+}
+
+}  // namespace
+
+dsc_status dsc_kv_append(void *stream, int dtype, int64_t N, int32_t n_seqs, int32_t Hq, int32_t Hkv,
+                         int32_t head_dim, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                         const void *v, int64_t v_stride, const int32_t *cu_seqlens, const int32_t *start,
+                         const float *table, int64_t max_pos, void *k_cache, void *v_cache, int64_t num_pages,
+                         int32_t page_size, const int32_t *page_table, int64_t max_pages, void *q_out) {
+    DSC_TRY(check_heads(dtype, Hq, Hkv, head_dim));
+    if (N < 0 || N > INT32_MAX - 512) return fail(DSC_ERR_SHAPE, "N = %lld tokens out of range", (long long)N);
+    if (n_seqs < 0) return fail(DSC_ERR_SHAPE, "n_seqs = %d out of range", n_seqs);
+    DSC_TRY(check_cache(n_seqs, Hkv, head_dim, num_pages, page_size, max_pages));
+    if (!cu_seqlens && N != n_seqs)
+        return fail(DSC_ERR_SHAPE, "without cu_seqlens every sequence gets one token (N = %lld, n_seqs = %d)", (long long)N,
+                    n_seqs);
+    if (N > 0 && n_seqs == 0) return fail(DSC_ERR_SHAPE, "%lld tokens of no sequence", (long long)N);
+    DSC_TRY(check_stride("k", dtype, k_stride, Hkv, head_dim));
+    DSC_TRY(check_stride("v", dtype, v_stride, Hkv, head_dim));
+    if ((q == nullptr) != (q_out == nullptr)) return fail(DSC_ERR_NULL, "q and q_out go together");
+    if (q) DSC_TRY(check_stride("q", dtype, q_stride, Hq, head_dim));
+    if (table && head_dim % 2) return fail(DSC_ERR_SHAPE, "head_dim = %d must be even to rotate", head_dim);
+    if (table && (max_pos < 1 || max_pos > INT32_MAX)) return fail(DSC_ERR_SHAPE, "max_pos = %lld out of range", (long long)max_pos);
+    if (N == 0) return ok();
+    if (!k || !v || !start || !page_table) return fail(DSC_ERR_NULL, "k, v, start and page_table are required");
+    if (num_pages > 0 && (!k_cache || !v_cache)) return fail(DSC_ERR_NULL, "k_cache and v_cache are required");
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(k_cache) ||
+        !aligned16(v_cache) || !aligned16(table))
+        return fail(DSC_ERR_ALIGNMENT, "pointers must be 16-byte aligned");
+    if (((uintptr_t)cu_seqlens | (uintptr_t)start | (uintptr_t)page_table) & 3u)
+        return fail(DSC_ERR_ALIGNMENT, "cu_seqlens, start and page_table must be 4-byte aligned");
+    const size_t es = esize(dtype), Ns = (size_t)N, S = (size_t)n_seqs;
+    const int64_t qw = (int64_t)Hq * head_dim, kw = (int64_t)Hkv * head_dim;
+    const size_t cb = (size_t)num_pages * page_size * kw * es;
+    const Rows in[] = {rows("q", q, q ? Ns : 0, q_stride, qw, es), rows("k", k, Ns, k_stride, kw, es),
+                       rows("v", v, Ns, v_stride, kw, es), flat("cu_seqlens", cu_seqlens, cu_seqlens ? 4u * (S + 1) : 0),
+                       flat("start", start, 4u * S), flat("page_table", page_table, 4u * S * (size_t)max_pages),
+                       flat("table", table, table ? (size_t)max_pos * head_dim * 4u : 0)};
+    const Rows out[] = {flat("k_cache", k_cache, cb), flat("v_cache", v_cache, cb),
+                        rows("q_out", q_out, q_out ? Ns : 0, qw, qw, es)};
+    DSC_TRY(check_rows(in, 7, out, 3));
+    dsc::AppendProblem p{};
+    p.dtype = dtype == DSC_BF16 ? dsc::Dtype::BF16 : dsc::Dtype::F32;
+    p.N = N, p.S = n_seqs, p.Hq = Hq, p.cu = cu_seqlens, p.start = start;
+    p.q = q, p.k = k, p.v = v, p.qs = q_stride, p.ks = k_stride, p.vs = v_stride, p.q_out = q_out;
+    p.rope = table, p.max_pos = table ? max_pos : 0;
+    p.c = dsc::PagedCache{k_cache, v_cache, page_table, num_pages, max_pages, page_size, Hkv, head_dim};
+    return launched(dsc::kv_append(p, (hipStream_t)stream), "dsc_kv_append launch");
+}
+
+namespace {
+
+dsc_status check_attn_decode(int dtype, int64_t S, int32_t Hq, int32_t Hkv, int32_t hd, int64_t num_pages,
+                             int32_t page_size, int64_t max_pages) {
+    DSC_TRY(check_heads(dtype, Hq, Hkv, hd));
+    DSC_TRY(check_cache(S, Hkv, hd, num_pages, page_size, max_pages));
+    if (S > 0 && Hq > (1 << 20) / S) return fail(DSC_ERR_SHAPE, "S * Hq must be at most 2^20 (S = %lld)", (long long)S);
+    return DSC_SUCCESS;
+}
+
+}  // namespace
+
+size_t dsc_attn_decode_workspace_size(int dtype, int64_t S, int32_t Hq, int32_t Hkv, int32_t head_dim,
+                                      int32_t page_size, int64_t max_pages) {
+    if (check_attn_decode(dtype, S, Hq, Hkv, head_dim, 0, page_size, max_pages) != DSC_SUCCESS) return 0;
+    return dsc::attn_decode_workspace(S, Hq, Hkv, head_dim, page_size, max_pages);
+}
+
+dsc_status dsc_attn_decode(void *stream, int dtype, int64_t S, int32_t Hq, int32_t Hkv, int32_t head_dim,
+                           const void *q, int64_t q_stride, const void *k_cache, const void *v_cache,
+                           int64_t num_pages, int32_t page_size, const int32_t *page_table, int64_t max_pages,
+                           const int32_t *lens, float scale, void *o, void *workspace, size_t workspace_bytes) {
+    DSC_TRY(check_attn_decode(dtype, S, Hq, Hkv, head_dim, num_pages, page_size, max_pages));
+    DSC_TRY(check_scale(scale));
+    DSC_TRY(check_stride("q", dtype, q_stride, Hq, head_dim));
+    if (S == 0) return ok();
+    if (!q || !page_table || !lens || !o) return fail(DSC_ERR_NULL, "q, page_table, lens and o are required");
+    if (num_pages > 0 && (!k_cache || !v_cache)) return fail(DSC_ERR_NULL, "k_cache and v_cache are required");
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o) || !aligned16(workspace))
+        return fail(DSC_ERR_ALIGNMENT, "pointers must be 16-byte aligned");
+    if (((uintptr_t)page_table | (uintptr_t)lens) & 3u)
+        return fail(DSC_ERR_ALIGNMENT, "page_table and lens must be 4-byte aligned");
+    const size_t need = dsc::attn_decode_workspace(S, Hq, Hkv, head_dim, page_size, max_pages);
+    if (need && (!workspace || workspace_bytes < need))
+        return fail(DSC_ERR_WORKSPACE, "workspace of %zu bytes required (got %zu)", need, workspace ? workspace_bytes : 0);
+    const size_t es = esize(dtype), Ss = (size_t)S;
+    const int64_t qw = (int64_t)Hq * head_dim;
+    const size_t cb = (size_t)num_pages * page_size * Hkv * head_dim * es;
+    const Rows in[] = {rows("q", q, Ss, q_stride, qw, es), flat("k_cache", k_cache, cb), flat("v_cache", v_cache, cb),
+                       flat("page_table", page_table, 4u * Ss * (size_t)max_pages), flat("lens", lens, 4u * Ss)};
+    const Rows out[] = {rows("o", o, Ss, qw, qw, es), flat("workspace", workspace, need)};
+    DSC_TRY(check_rows(in, 5, out, 2));
+    dsc::AttnDecodeProblem p{};
+    p.dtype = dtype == DSC_BF16 ? dsc::Dtype::BF16 : dsc::Dtype::F32;
+    p.S = S, p.Hq = Hq, p.q = q, p.qs = q_stride, p.lens = lens, p.scale = scale, p.o = o, p.ws = workspace;
+    p.c = dsc::PagedCache{const_cast<void *>(k_cache), const_cast<void *>(v_cache), page_table, num_pages, max_pages,
+                          page_size, Hkv, head_dim};
+    return launched(dsc::attn_decode(p, (hipStream_t)stream), "dsc_attn_decode launch");
+}
+
 dsc_status dsc_bench_stream(void *stream, const void *src, int64_t read_bytes, void *dst, int64_t write_bytes,
                             int32_t unroll, int32_t load_nt, int32_t store_nt, int32_t chunked, int64_t blocks) {
     const int64_t kMax = (int64_t)1 << 40;

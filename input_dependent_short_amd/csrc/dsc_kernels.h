@@ -174,6 +174,67 @@ hipError_t noalloc_scratch(float **out);
 hipError_t stream_probe(const void *src, int64_t read_bytes, void *dst, int64_t write_bytes, int unroll, bool lnt,
                         bool snt, bool chunked, int64_t blocks, hipStream_t s);
 
+// Causal attention over whole prompts (attn_fwd.hip, attn_bwd.hip): token rows
+// of q, k, v (and dq, dk, dv) are qs, ks, vs (dqs, dks, dvs) elements apart,
+// heads hd; o and dout are dense (N, Hq*hd), lse (Hq, N).
+struct AttnProblem {
+    Dtype dtype;
+    int64_t N, T;
+    int32_t Hq, Hkv, hd;
+    const void *q, *k, *v;
+    int64_t qs, ks, vs;
+    const int32_t *cu;
+    int32_t n_seqs;
+    float scale;
+    void *o;
+    float *lse;
+    const void *dout;  // backward only, from here
+    void *dq, *dk, *dv;
+    int64_t dqs, dks, dvs;
+    void *ws;  // attn_bwd_workspace bytes
+};
+hipError_t attn_fwd(const AttnProblem &p, hipStream_t s);
+size_t attn_bwd_workspace(int64_t N, int32_t Hq);
+hipError_t attn_bwd(const AttnProblem &p, hipStream_t s);
+
+// A paged cache: k, v (num_pages, Hkv, page, hd), pages (S, max_pages) int32.
+struct PagedCache {
+    void *k, *v;
+    const int32_t *pages;
+    int64_t num_pages, max_pages;
+    int32_t page, Hkv, hd;
+};
+// New tokens into the cache (kv_cache.hip): token n of sequence s goes to
+// position start[s] + its index in the call; cu null: one token per sequence.
+struct AppendProblem {
+    Dtype dtype;
+    int64_t N;
+    int32_t S, Hq;
+    const int32_t *cu, *start;
+    const void *q, *k, *v;  // q, q_out null: keys and values only
+    int64_t qs, ks, vs;
+    void *q_out;
+    const float *rope;  // (max_pos, hd/2, 2), null: no rotation
+    int64_t max_pos;
+    PagedCache c;
+};
+hipError_t kv_append(const AppendProblem &p, hipStream_t s);
+// One new token per sequence over the cache (attn_decode.hip).
+struct AttnDecodeProblem {
+    Dtype dtype;
+    int64_t S;
+    int32_t Hq;
+    const void *q;
+    int64_t qs;
+    const int32_t *lens;
+    float scale;
+    void *o;
+    PagedCache c;
+    void *ws;  // attn_decode_workspace bytes
+};
+size_t attn_decode_workspace(int64_t S, int32_t Hq, int32_t Hkv, int32_t hd, int32_t page, int64_t max_pages);
+hipError_t attn_decode(const AttnDecodeProblem &p, hipStream_t s);
+
 // Zero-fills n fp32 values (16-byte aligned); the backward of an empty batch.
 hipError_t lowrank_zero(float *p, int64_t n, hipStream_t s);
 // Zeroes two fp32 arrays in one launch; rounds n fp32 values to bf16.

@@ -1,0 +1,119 @@
+// kv_cache.hip -- new tokens' keys and values into a paged cache, keys (and
+// queries) turned by the rotary embedding on the way, for gfx950.  The
+// rotation is that of rope.hip: pair i (channels 2i, 2i+1) of a head turns by
+// position * theta_i, cos and sin from the fp32 table.
+//
+// The call only moves bytes: one 16-byte chunk per thread and step, read from
+// the token's [Q | K | V] row and written once.  A block takes a few tokens
+// (their sequence, position and page are looked up once per block and kept in
+// LDS) and a slice of the row's chunks; with few tokens the row is cut finer,
+// so that a decoding step still spreads over the device.
+#include <algorithm>
+
+#include "dsc_common.h"
+#include "dsc_kernels.h"
+
+namespace dsc {
+namespace {
+
+constexpr int kMaxTok = 4;  // tokens per block
+
+struct AppParams {
+    const void *q, *k, *v;
+    void *q_out, *kc, *vc;
+    const int32_t *cu, *start, *pages;
+    const float *rope;
+    int64_t N, qs, ks, vs, num_pages, max_pages, max_pos;
+    int32_t S, Hq, Hkv, hd, page, ntok, slice;
+};
+
+template <class E>
+__global__ __launch_bounds__(256) void kv_append_kernel(AppParams p) {
+    using T = typename E::store_t;
+    constexpr int VEC = E::kVec;
+    __shared__ int64_t slot_s[kMaxTok];  // row of the (page, head 0) cache, or -1
+    __shared__ int32_t pos_s[kMaxTok];
+    const int64_t n0 = (int64_t)blockIdx.x * p.ntok;
+    if ((int)threadIdx.x < p.ntok && n0 + threadIdx.x < p.N) {
+        const int64_t n = n0 + threadIdx.x;
+        int s = (int)n;
+        int64_t idx = 0;
+        if (p.cu) {
+            int lo = 0, hi = p.S;  // cu[lo] <= n < cu[hi]
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if ((int64_t)p.cu[mid] <= n) lo = mid;
+                else hi = mid;
+            }
+            s = lo;
+            idx = n - p.cu[lo];
+        }
+        const int64_t pos = (int64_t)p.start[s] + idx;
+        int64_t slot = -1;
+        if (pos >= 0 && pos < p.max_pages * p.page) {
+            const int32_t pg = p.pages[(int64_t)s * p.max_pages + pos / p.page];
+            if (pg >= 0 && pg < p.num_pages) slot = (int64_t)pg * p.Hkv * p.page + pos % p.page;
+        }
+        slot_s[threadIdx.x] = slot;
+        pos_s[threadIdx.x] = pos >= 0 && pos < p.max_pos ? (int32_t)pos : -1;
+    }
+    __syncthreads();
+
+    const uint32_t cph = (uint32_t)p.hd / VEC;  // chunks per head
+    const uint32_t nq = p.q ? (uint32_t)p.Hq : 0u;
+    const uint32_t total = (nq + 2u * (uint32_t)p.Hkv) * cph;
+    const uint32_t c0 = blockIdx.y * (uint32_t)p.slice, c1 = min(total, c0 + (uint32_t)p.slice);
+    for (int t = 0; t < p.ntok && n0 + t < p.N; ++t) {
+        const int64_t n = n0 + t, slot = slot_s[t];
+        const int32_t pos = pos_s[t];
+        for (uint32_t c = c0 + threadIdx.x; c < c1; c += 256) {
+            const uint32_t head = c / cph, off = (c - head * cph) * VEC;
+            const bool is_q = head < nq, is_v = head >= nq + (uint32_t)p.Hkv;
+            const uint32_t hh = is_q ? head : head - nq - (is_v ? (uint32_t)p.Hkv : 0u);
+            if (!is_q && slot < 0) continue;
+            const T *src = is_q   ? static_cast<const T *>(p.q) + n * p.qs
+                           : is_v ? static_cast<const T *>(p.v) + n * p.vs
+                                  : static_cast<const T *>(p.k) + n * p.ks;
+            src += (int64_t)hh * p.hd + off;
+            T *dst = is_q ? static_cast<T *>(p.q_out) + (n * p.Hq + hh) * p.hd + off
+                          : static_cast<T *>(is_v ? p.vc : p.kc) + (slot + (int64_t)hh * p.page) * p.hd + off;
+            if (is_v || !p.rope) {
+                *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<const uint4 *>(src);
+                continue;
+            }
+            float v[VEC], cs[VEC];
+            Vec16<E>::load(src, v);
+            if (pos >= 0) {
+                load_turn<VEC>(p.rope + (int64_t)pos * p.hd + off, cs);
+            } else {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) cs[i] = __builtin_nanf("");
+            }
+            turn<VEC, false>(v, cs);
+            Vec16<E>::store(dst, v);
+        }
+    }
+}
+
+}  // namespace
+
+hipError_t kv_append(const AppendProblem &a, hipStream_t s) {
+    const int vec = a.dtype == Dtype::BF16 ? 8 : 4;
+    const int chunks = ((a.q ? a.Hq : 0) + 2 * a.c.Hkv) * (a.c.hd / vec);
+    // Enough blocks for every CU first by tokens, then by slices of the row.
+    const int64_t want = 4 * (int64_t)device_cus();
+    int ntok = (int)std::min<int64_t>(kMaxTok, std::max<int64_t>(1, a.N / want));
+    const int64_t bx = (a.N + ntok - 1) / ntok;
+    int cuts = (int)std::min<int64_t>((chunks + 255) / 256, std::max<int64_t>(1, want / bx));
+    int slice = (chunks + cuts - 1) / cuts;
+    cuts = (chunks + slice - 1) / slice;
+    AppParams p{a.q, a.k, a.v, a.q_out, a.c.k, a.c.v, a.cu, a.start, a.c.pages, a.rope, a.N, a.qs, a.ks, a.vs,
+                a.c.num_pages, a.c.max_pages, a.max_pos, a.S, a.Hq, a.c.Hkv, a.c.hd, a.c.page, ntok, slice};
+    if (a.dtype == Dtype::BF16)
+        hipLaunchKernelGGL((kv_append_kernel<BF16>), dim3((unsigned)bx, (unsigned)cuts), dim3(256), 0, s, p);
+    else
+        hipLaunchKernelGGL((kv_append_kernel<F32>), dim3((unsigned)bx, (unsigned)cuts), dim3(256), 0, s, p);
+    return hipGetLastError();
+}
+
+}  // namespace dsc

@@ -1,0 +1,125 @@
+"""Argument checks of the attention and cache calls (CPU only: every call fails validation before any HIP call)."""
+import ctypes
+
+import pytest
+import torch
+
+from input_dependent_short_amd import binding
+
+A = 1 << 32
+P = lambda k, off=0: ctypes.c_void_p(A * k + off)
+S0 = ctypes.c_void_p(0)
+OK, NULL, SHAPE, UNSUP, ALIGN, ALIAS, WS = range(7)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return binding.lib()
+
+
+def fwd(lib, dt=1, B=1, T=8, Hq=4, Hkv=2, hd=64, q=P(1), qs=512, k=P(2), ks=512, v=P(3), vs=512, cu=None, ns=0,
+        scale=0.1, o=P(4), lse=P(5)):
+    return lib.dsc_attn_fwd(S0, dt, B, T, Hq, Hkv, hd, q, qs, k, ks, v, vs, cu, ns, scale, o, lse)
+
+
+def test_attn_fwd_refusals(lib):
+    assert fwd(lib, dt=5) == UNSUP and fwd(lib, hd=136) == UNSUP and fwd(lib, hd=60) == UNSUP
+    assert fwd(lib, dt=0, hd=62) == UNSUP and fwd(lib, hd=0) == SHAPE
+    assert fwd(lib, Hq=3) == SHAPE and fwd(lib, Hkv=0) == SHAPE and fwd(lib, Hq=0) == SHAPE
+    assert fwd(lib, B=-1) == SHAPE and fwd(lib, B=1 << 40, T=1 << 40) == SHAPE and fwd(lib, B=1, T=2 ** 31 - 1) == SHAPE
+    assert fwd(lib, qs=248) == SHAPE and fwd(lib, ks=124) == SHAPE and fwd(lib, vs=130) == SHAPE
+    assert fwd(lib, qs=1 << 21) == SHAPE and fwd(lib, ks=-512) == SHAPE
+    for s in (0.0, -1.0, float("inf"), float("nan")):
+        assert fwd(lib, scale=s) == SHAPE
+    assert fwd(lib, cu=P(9), ns=0) == SHAPE and fwd(lib, ns=2) == SHAPE and fwd(lib, cu=P(9), ns=9) == SHAPE
+    assert fwd(lib, q=None) == NULL and fwd(lib, o=None) == NULL
+    assert fwd(lib, q=P(1, 8)) == ALIGN and fwd(lib, lse=P(5, 4)) == ALIGN
+    assert fwd(lib, o=P(1)) == ALIAS and fwd(lib, o=P(4), lse=P(4, 64)) == ALIAS
+    assert fwd(lib, cu=P(4), ns=2) == ALIAS
+    # views of one row: o within the row's bytes is an overlap
+    assert fwd(lib, q=P(1), k=P(1, 512), v=P(1, 768), o=P(1, 1024 * 7)) == ALIAS
+    assert b"overlaps" in lib.dsc_last_error()
+
+
+def bwd(lib, hd=64, q=P(1), qs=512, k=P(2), v=P(3), o=P(4), lse=P(5), g=P(6), dq=P(7), dqs=512, dk=P(8), dks=512,
+        dv=P(9), dvs=512, ws=P(10), wsb=1 << 20, T=8):
+    return lib.dsc_attn_bwd(S0, 1, 1, T, 4, 2, hd, q, qs, k, 512, v, 512, o, lse, g, None, 0, 0.1, dq, dqs, dk, dks,
+                            dv, dvs, ws, wsb)
+
+
+def test_attn_bwd_refusals(lib):
+    need = lib.dsc_attn_bwd_workspace_size(1, 1, 8, 4, 2, 64)
+    assert need == 2 * 4 * 8 * 4
+    assert lib.dsc_attn_bwd_workspace_size(1, 1, 8, 4, 3, 64) == 0
+    assert lib.dsc_attn_bwd_workspace_size(1, 1 << 40, 1 << 40, 4, 2, 64) == 0
+    assert bwd(lib, wsb=need - 1) == WS and bwd(lib, ws=None) == WS
+    assert bwd(lib, lse=None) == NULL and bwd(lib, dv=None) == NULL
+    assert bwd(lib, g=P(6, 2)) == ALIGN
+    assert bwd(lib, dqs=128) == SHAPE and bwd(lib, dks=129) == SHAPE
+    assert bwd(lib, dq=P(1)) == ALIAS and bwd(lib, dk=P(9)) == ALIAS and bwd(lib, ws=P(7, 64)) == ALIAS
+    # dq, dk, dv of one row interleave without sharing a byte: that passes, so the next check (the workspace,
+    # placed over dv) is the one that refuses; one channel of overlap is refused
+    assert bwd(lib, dq=P(7), dk=P(7, 512), dv=P(7, 768), ws=P(7, 768)) == ALIAS
+    assert b"dv and workspace" in lib.dsc_last_error()
+    assert bwd(lib, dq=P(7), dk=P(7, 496), dv=P(7, 768)) == ALIAS
+    assert b"dq and dk" in lib.dsc_last_error()
+    assert bwd(lib, dq=P(7, 528), dk=P(7, 256), dv=P(7)) == ALIAS          # dq's tail wraps into the next row's dv
+    # an empty batch computes nothing
+    assert bwd(lib, T=0, q=None, ws=None) == OK
+
+
+def append(lib, dt=1, N=4, S=4, Hq=4, Hkv=2, hd=64, q=P(1), qs=256, k=P(2), ks=128, v=P(3), vs=128, cu=None,
+           start=P(4), tab=P(5), mp=100, kc=P(6), vc=P(7), pages=10, page=16, pt=P(8), maxp=5, qo=P(9)):
+    return lib.dsc_kv_append(S0, dt, N, S, Hq, Hkv, hd, q, qs, k, ks, v, vs, cu, start, tab, mp, kc, vc, pages, page,
+                             pt, maxp, qo)
+
+
+def test_kv_append_refusals(lib):
+    assert append(lib, dt=3) == UNSUP and append(lib, hd=20) == UNSUP
+    assert append(lib, N=5) == SHAPE and append(lib, N=-1) == SHAPE and append(lib, S=-1, N=0) == SHAPE
+    assert append(lib, S=0, N=3, cu=P(10)) == SHAPE
+    assert append(lib, page=0) == SHAPE and append(lib, maxp=0) == SHAPE and append(lib, maxp=1 << 30) == SHAPE
+    assert append(lib, pages=-1) == SHAPE and append(lib, pages=1 << 40) == SHAPE
+    assert append(lib, mp=0) == SHAPE and append(lib, ks=120) == SHAPE
+    assert append(lib, q=None) == NULL and append(lib, qo=None) == NULL and append(lib, start=None) == NULL
+    assert append(lib, kc=None) == NULL
+    assert append(lib, pt=P(8, 2)) == ALIGN and append(lib, vc=P(7, 8)) == ALIGN
+    assert append(lib, kc=P(7)) == ALIAS and append(lib, qo=P(1)) == ALIAS and append(lib, kc=P(2)) == ALIAS
+    assert append(lib, N=0, S=0, q=None, qo=None, k=None) == OK
+
+
+def dec(lib, dt=1, S=4, Hq=4, Hkv=2, hd=64, q=P(1), qs=256, kc=P(2), vc=P(3), pages=10, page=16, pt=P(4), maxp=500,
+        lens=P(5), scale=0.1, o=P(6), ws=P(7), wsb=1 << 40):
+    return lib.dsc_attn_decode(S0, dt, S, Hq, Hkv, hd, q, qs, kc, vc, pages, page, pt, maxp, lens, scale, o, ws, wsb)
+
+
+def test_attn_decode_refusals(lib):
+    assert dec(lib, dt=9) == UNSUP and dec(lib, hd=256) == UNSUP and dec(lib, Hkv=3) == SHAPE
+    assert dec(lib, S=-1) == SHAPE and dec(lib, S=1 << 20) == SHAPE and dec(lib, scale=0.0) == SHAPE
+    assert dec(lib, qs=8) == SHAPE and dec(lib, page=-1) == SHAPE and dec(lib, maxp=0) == SHAPE
+    need = lib.dsc_attn_decode_workspace_size(1, 4, 4, 2, 64, 16, 500)
+    assert need > 0 and lib.dsc_attn_decode_workspace_size(1, 4, 4, 3, 64, 16, 500) == 0
+    assert dec(lib, wsb=need - 1) == WS and dec(lib, ws=None) == WS
+    assert dec(lib, lens=None) == NULL and dec(lib, vc=None) == NULL
+    assert dec(lib, lens=P(5, 1)) == ALIGN and dec(lib, q=P(1, 4)) == ALIGN
+    assert dec(lib, o=P(1)) == ALIAS and dec(lib, o=P(2)) == ALIAS and dec(lib, ws=P(3)) == ALIAS
+    assert dec(lib, S=0, q=None) == OK
+
+
+def test_binding_refusals():
+    q = torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16)
+    k = torch.zeros(1, 4, 1, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        binding.dsc_attn_fwd(q, k, k[:, :3], q)
+    with pytest.raises(TypeError):
+        binding.dsc_attn_fwd(q, k.float(), k.float(), q)
+    with pytest.raises(ValueError):  # channels not contiguous
+        binding.dsc_attn_fwd(q.transpose(2, 3).contiguous().transpose(2, 3), k, k, q)
+    with pytest.raises(ValueError):  # rows of another spacing between batches
+        binding.dsc_attn_fwd(torch.zeros(2, 9, 2, 64)[:, :4], torch.zeros(2, 4, 1, 64), torch.zeros(2, 4, 1, 64),
+                             torch.zeros(2, 4, 2, 64))
+    with pytest.raises(ValueError):
+        binding.dsc_kv_append(k[0], k[0], torch.zeros(3, 2, 8, 64, dtype=k.dtype), torch.zeros(3, 2, 8, 64, dtype=k.dtype),
+                              torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, dtype=torch.int32))
+    with pytest.raises(TypeError):
+        binding.dsc_attn_decode(q[0], k, k, torch.zeros(4, 2, dtype=torch.int64), torch.zeros(4, dtype=torch.int32), q[0])

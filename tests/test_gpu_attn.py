@@ -1,0 +1,375 @@
+"""Attention over prompts, the paged cache and decoding over it, on the GPU, against fp64 (tests/attn_ref.py).
+
+Every output element is held to the bound that the reference derives for it.
+"""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import attn_ref
+from gpu_util import say
+from input_dependent_short_amd import binding
+from input_dependent_short_amd.inputs import DTYPES, to_f64
+
+pytestmark = pytest.mark.gpu
+
+POISON = -1536.0  # exact in bf16
+
+
+def within(name, got, ref):
+    val, bound = ref
+    got = to_f64(got) if isinstance(got, torch.Tensor) else got
+    assert got.shape == val.shape, (name, got.shape, val.shape)
+    assert np.isfinite(got).all(), f"{name}: not finite"
+    over = np.abs(got - val) / bound
+    say(f"    {name}: worst {over.max() if over.size else 0:.3f} of its bound")
+    assert (over <= 1.0).all(), f"{name}: {over.max():.3g} times its bound at {np.unravel_index(over.argmax(), over.shape)}"
+
+
+def qkv(B, T, Hq, Hkv, hd, dtype, seed, layout="packed", pad=0, gain=1.4):
+    """q, k, v views of one [Q | K | V] row (pad extra channels behind it) or dense tensors, on the GPU."""
+    r = np.random.default_rng(seed)
+    w = (Hq + 2 * Hkv) * hd + pad
+    x = torch.from_numpy(r.standard_normal((B, T, w), dtype=np.float32))
+    x[..., :(Hq + Hkv) * hd] *= gain
+    row = x.to(DTYPES[dtype]).cuda()
+    q, k, v = row[..., :Hq * hd], row[..., Hq * hd:(Hq + Hkv) * hd], row[..., (Hq + Hkv) * hd:(Hq + 2 * Hkv) * hd]
+    q, k, v = q.unflatten(-1, (Hq, hd)), k.unflatten(-1, (Hkv, hd)), v.unflatten(-1, (Hkv, hd))
+    if layout == "dense":
+        q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+    return row, q, k, v
+
+
+def cu_of(lens):
+    return None if lens is None else torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32).cuda()
+
+
+def run(q, k, v, g, cu, scale, layout="packed"):
+    """o, lse and the gradients, written into poisoned outputs."""
+    B, T, Hq, hd = q.shape
+    Hkv = k.shape[2]
+    o = torch.full((B, T, Hq, hd), POISON, dtype=q.dtype, device="cuda")
+    lse = torch.full((Hq, B * T), POISON, dtype=torch.float32, device="cuda")
+    binding.dsc_attn_fwd(q, k, v, o, lse, scale=scale, cu_seqlens=cu)
+    out = {"o": o, "lse": lse}
+    if g is not None:
+        if layout == "packed":
+            d = torch.full((B, T, (Hq + 2 * Hkv) * hd + 8), POISON, dtype=q.dtype, device="cuda")
+            dq, dk, dv = (d[..., a * hd:b * hd].unflatten(-1, (b - a, hd)) for a, b in
+                          ((0, Hq), (Hq, Hq + Hkv), (Hq + Hkv, Hq + 2 * Hkv)))
+        else:
+            dq, dk, dv = (torch.full_like(x, POISON) for x in (q, k, v))
+        n = binding.dsc_attn_bwd_workspace_size(q.dtype, B, T, Hq, Hkv, hd)
+        ws = torch.full((n // 4,), float("nan"), device="cuda")
+        binding.dsc_attn_bwd(q, k, v, o, lse, g, dq, dk, dv, ws, scale=scale, cu_seqlens=cu)
+        out.update(dq=dq, dk=dk, dv=dv)
+        if layout == "packed":
+            assert (d[..., (Hq + 2 * Hkv) * hd:] == POISON).all(), "channels behind the row were written"
+    torch.cuda.synchronize()
+    return out
+
+
+def flat64(x):
+    return to_f64(x.flatten(0, 1))
+
+
+# dtype, B, T, Hq, Hkv, hd, lengths (None: rows), layout
+PROMPTS = [
+    ("bf16", 1, 1, 1, 1, 64, None, "dense"),
+    ("bf16", 1, 37, 12, 12, 64, None, "packed"),
+    ("bf16", 2, 128, 4, 2, 128, None, "packed"),
+    ("bf16", 2, 129, 4, 1, 128, None, "dense"),
+    ("bf16", 1, 300, 6, 2, 96, [1, 1, 31, 32, 33, 0, 64, 65, 73], "packed"),
+    ("bf16", 3, 200, 3, 3, 80, [150, 100, 1, 349], "packed"),
+    ("bf16", 1, 513, 2, 1, 8, [255, 258], "dense"),
+    ("bf16", 1, 700, 8, 1, 40, None, "packed"),
+    ("bf16", 1, 257, 7, 1, 72, [1] * 57 + [100, 100], "packed"),
+    ("fp32", 1, 1, 2, 1, 4, None, "dense"),
+    ("fp32", 2, 63, 3, 3, 64, None, "packed"),
+    ("fp32", 1, 301, 6, 2, 80, [1, 130, 2, 168], "packed"),
+    ("fp32", 2, 160, 4, 1, 128, [33, 255, 32], "dense"),
+    ("fp32", 1, 257, 2, 2, 12, None, "packed"),
+    ("fp32", 1, 130, 5, 1, 100, [64, 66], "packed"),
+]
+
+
+@pytest.mark.parametrize("dtype,B,T,Hq,Hkv,hd,lens,layout", PROMPTS)
+def test_prompt_and_gradients(dtype, B, T, Hq, Hkv, hd, lens, layout):
+    say(f"[attn] {dtype} B={B} T={T} Hq={Hq} Hkv={Hkv} hd={hd} lens={lens} {layout}")
+    _, q, k, v = qkv(B, T, Hq, Hkv, hd, dtype, 100 + T, layout)
+    g = torch.from_numpy(np.random.default_rng(T).standard_normal((B, T, Hq, hd), dtype=np.float32)).to(q.dtype).cuda()
+    scale = hd ** -0.5
+    got = run(q, k, v, g, cu_of(lens), scale, layout)
+    cu = None if lens is None else np.concatenate([[0], np.cumsum(lens)])
+    ref = attn_ref.full(flat64(q), flat64(k), flat64(v), flat64(g), float(np.float32(scale)),
+                        attn_ref.segments(B, T, cu), dtype)
+    within("o", flat64(got["o"]), ref["o"])
+    within("lse", got["lse"], ref["lse"])
+    for n in ("dq", "dk", "dv"):
+        within(n, flat64(got[n]), ref[n])
+
+
+def test_scores_of_large_range():
+    """Scores of several hundred: the running maximum carries the softmax, early keys vanish."""
+    for dtype in ("bf16", "fp32"):
+        _, q, k, v = qkv(1, 200, 2, 1, 64, dtype, 3, gain=8.0)
+        got = run(q, k, v, None, None, 1.0)
+        o, lse = attn_ref.forward(flat64(q), flat64(k), flat64(v), 1.0, [(0, 200)])
+        # probabilities carry the scores' error: 1e-6 of sums of |q||k| near 4000, exponentiated
+        assert np.max(np.abs(flat64(got["o"]) - o)) < 3e-2
+        assert np.max(np.abs(to_f64(got["lse"]) - lse)) < 1e-5 * np.max(np.abs(lse)) + 4e-3
+
+
+def test_gradients_against_differences():
+    """<dx, u> of the kernel's gradients against central differences of the fp64 loss along u."""
+    B, T, Hq, Hkv, hd, scale = 1, 150, 4, 2, 64, 0.2
+    _, q, k, v = qkv(B, T, Hq, Hkv, hd, "fp32", 21)
+    r = np.random.default_rng(4)
+    g = torch.from_numpy(r.standard_normal((B, T, Hq, hd), dtype=np.float32)).cuda()
+    cu = [0, 40, 41, 150]
+    got = run(q, k, v, g, torch.tensor(cu, dtype=torch.int32).cuda(), scale)
+    x = [flat64(t) for t in (q, k, v)]
+    g64, segs = flat64(g), attn_ref.segments(B, T, cu)
+    bounds = attn_ref.full(*x, g64, float(np.float32(scale)), segs, "fp32")
+    loss = lambda: float(np.sum(g64 * attn_ref.forward(*x, float(np.float32(scale)), segs)[0]))
+    for i, n in enumerate(("dq", "dk", "dv")):
+        u = r.standard_normal(x[i].shape)
+        keep = x[i]
+        x[i] = keep + 1e-5 * u
+        up = loss()
+        x[i] = keep - 1e-5 * u
+        num = (up - loss()) / 2e-5
+        x[i] = keep
+        assert abs(num - float(np.sum(flat64(got[n]) * u))) <= float(np.sum(bounds[n][1] * np.abs(u))) + 1e-5
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_what_a_row_must_not_see(dtype, bad):
+    """A token of non-finite q, k, v and g changes neither earlier rows of its sequence nor other sequences."""
+    lens, at = [50, 70, 100], 50 + 33
+    scale = 0.125
+    row, q, k, v = qkv(1, 220, 4, 2, 64, dtype, 31)
+    g = torch.from_numpy(np.random.default_rng(8).standard_normal((1, 220, 4, 64), dtype=np.float32)).to(q.dtype).cuda()
+    clean = run(q, k, v, g, cu_of(lens), scale)
+    clean = {n: t.clone() for n, t in clean.items()}
+    row[0, at] = bad
+    g[0, at] = bad
+    got = run(q, k, v, g, cu_of(lens), scale)
+    assert torch.equal(got["o"][0, :at], clean["o"][0, :at]) and torch.equal(got["o"][0, 120:], clean["o"][0, 120:])
+    assert torch.equal(got["lse"][:, :at], clean["lse"][:, :at])
+    assert not torch.isfinite(got["o"][0, at]).any()
+    for n in ("dq", "dk", "dv"):
+        for a, b in ((0, 50), (120, 220)):
+            assert torch.equal(got[n][0, a:b], clean[n][0, a:b]), n
+    assert torch.equal(got["dq"][0, 50:at], clean["dq"][0, 50:at])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("bad", [float("nan"), float("-inf")])
+def test_gradient_rows_that_a_key_must_not_see(dtype, bad):
+    """One token's dL/do not finite: only its own dq, and dk, dv of the keys that it sees."""
+    at = 50 + 33
+    _, q, k, v = qkv(1, 220, 4, 2, 64, dtype, 33)
+    g = torch.from_numpy(np.random.default_rng(9).standard_normal((1, 220, 4, 64), dtype=np.float32)).to(q.dtype).cuda()
+    cu = cu_of([50, 70, 100])
+    clean = {n: t.clone() for n, t in run(q, k, v, g, cu, 0.125).items()}
+    g[0, at, 1, 3] = bad  # one channel of one head (of key head 0)
+    got = run(q, k, v, g, cu, 0.125)
+    for n in ("dk", "dv"):
+        for a, b in ((0, 50), (at + 1, 220)):
+            assert torch.equal(got[n][0, a:b], clean[n][0, a:b]), n
+    assert not torch.isfinite(got["dk"][0, 50:at + 1, 0]).any()
+    assert not torch.isfinite(got["dv"][0, 50:at + 1, 0, 3]).any()
+    keep = torch.ones(220, dtype=torch.bool, device="cuda")
+    keep[at] = False
+    assert torch.equal(got["dq"][0, keep], clean["dq"][0, keep])
+    assert torch.equal(got["dq"][0, at, 0], clean["dq"][0, at, 0]) and not torch.isfinite(got["dq"][0, at, 1]).any()
+
+
+def test_same_bits_every_time():
+    _, q, k, v = qkv(2, 400, 8, 2, 128, "bf16", 41)
+    g = torch.randn(2, 400, 8, 128, device="cuda").to(q.dtype)
+    a = {n: t.clone() for n, t in run(q, k, v, g, None, 0.1).items()}
+    for _ in range(3):
+        b = run(q, k, v, g, None, 0.1)
+        for n in a:
+            assert torch.equal(a[n], b[n]), n
+
+
+def test_without_lse_and_on_another_stream():
+    _, q, k, v = qkv(1, 333, 4, 4, 64, "bf16", 51)
+    want = run(q, k, v, None, None, 0.125)["o"]
+    s = torch.cuda.Stream()
+    o = torch.empty_like(want)
+    s.wait_stream(torch.cuda.current_stream())
+    binding.dsc_attn_fwd(q, k, v, o, stream=s)
+    s.synchronize()
+    assert torch.equal(o, want)
+
+
+# --------------------------------------------------------------- the cache
+
+def cache_case(lens, page, Hkv, hd, dtype, seed, width=None):
+    """Shuffled page table (unused entries invalid) and a pool whose unused places hold NaN."""
+    r = np.random.default_rng(seed)
+    need = [-(-n // page) for n in lens]
+    width = width or max(max(need), 1)
+    pool = sum(need) + 2
+    order = r.permutation(pool)
+    table, at = np.full((len(lens), width), -7, np.int32), 0
+    for i, n in enumerate(need):
+        table[i, :n] = order[at:at + n]
+        at += n
+    ks = [r.standard_normal((n, Hkv, hd)).astype(np.float32) * 1.4 for n in lens]
+    vs = [r.standard_normal((n, Hkv, hd)).astype(np.float32) for n in lens]
+    kc = torch.full((pool, Hkv, page, hd), float("nan"), dtype=DTYPES[dtype])
+    vc = torch.full((pool, Hkv, page, hd), float("nan"), dtype=DTYPES[dtype])
+    for i, n in enumerate(lens):
+        for t in range(0, n, page):
+            m = min(page, n - t)
+            pg = int(table[i, t // page])
+            kc[pg, :, :m] = torch.from_numpy(ks[i][t:t + m]).transpose(0, 1).to(kc.dtype)
+            vc[pg, :, :m] = torch.from_numpy(vs[i][t:t + m]).transpose(0, 1).to(vc.dtype)
+    rounded = lambda x: to_f64(torch.from_numpy(x).to(DTYPES[dtype]))
+    return torch.from_numpy(table).cuda(), kc.cuda(), vc.cuda(), [rounded(x) for x in ks], [rounded(x) for x in vs]
+
+
+def decode(q, kc, vc, table, lens, scale):
+    S, Hq, hd = q.shape
+    o = torch.full((S, Hq, hd), POISON, dtype=q.dtype, device="cuda")
+    n = binding.dsc_attn_decode_workspace_size(q.dtype, S, Hq, kc.shape[1], hd, kc.shape[2], table.shape[1])
+    ws = torch.full((max(n, 16) // 4,), float("nan"), device="cuda")
+    binding.dsc_attn_decode(q, kc, vc, table, lens, o, ws, scale=scale)
+    torch.cuda.synchronize()
+    return o
+
+
+# dtype, lengths, page, Hq, Hkv, hd
+DECODES = [
+    ("bf16", [1], 16, 1, 1, 64),
+    ("bf16", [777], 16, 12, 12, 64),
+    ("bf16", [0, 1, 31, 32, 33, 64, 65, 500], 16, 8, 2, 128),
+    ("bf16", [2000, 3, 0, 129], 48, 4, 1, 96),
+    ("bf16", [130, 257], 1, 3, 1, 40),
+    ("bf16", [300, 299], 7, 34, 1, 80),       # more heads of a group than one tile's 16 columns
+    ("bf16", [5000], 256, 16, 2, 128),
+    ("bf16", [4, 90] * 40, 24, 6, 3, 8),
+    ("fp32", [1, 16, 17, 0, 400], 16, 4, 2, 64),
+    ("fp32", [3000], 48, 16, 2, 128),
+    ("fp32", [100, 33], 5, 5, 5, 100),
+    ("fp32", [64] * 3, 64, 20, 1, 12),
+]
+
+
+@pytest.mark.parametrize("dtype,lens,page,Hq,Hkv,hd", DECODES)
+def test_decode(dtype, lens, page, Hq, Hkv, hd):
+    say(f"[attn decode] {dtype} lens={lens[:8]} page={page} Hq={Hq} Hkv={Hkv} hd={hd}")
+    table, kc, vc, ks, vs = cache_case(lens, page, Hkv, hd, dtype, len(lens) + page)
+    r = np.random.default_rng(6)
+    row = torch.from_numpy(r.standard_normal((len(lens), Hq * hd + 16), dtype=np.float32)).to(DTYPES[dtype]).cuda()
+    q = row[:, :Hq * hd].unflatten(-1, (Hq, hd))  # strided rows
+    scale = hd ** -0.5
+    o = decode(q, kc, vc, table, torch.tensor(lens, dtype=torch.int32).cuda(), scale)
+    within("o", o, attn_ref.decode(to_f64(q), ks, vs, float(np.float32(scale)), dtype))
+    for i, n in enumerate(lens):
+        if n == 0:
+            assert (o[i] == 0).all()
+
+
+def test_decode_of_lengths_far_below_the_table():
+    """The table allows 40,000 tokens, the sequences hold few: chunks past a length are left out of the join."""
+    lens, page = [5, 1300, 0], 64
+    table, kc, vc, ks, vs = cache_case(lens, page, 2, 64, "bf16", 77, width=40000 // page)
+    q = torch.randn(3, 4, 64, device="cuda").to(torch.bfloat16)
+    o = decode(q, kc, vc, table, torch.tensor(lens, dtype=torch.int32).cuda(), 0.125)
+    within("o", o, attn_ref.decode(to_f64(q), ks, vs, 0.125, "bf16"))
+
+
+def test_decode_reads_nothing_outside_the_pool():
+    """Lengths outside the table and page numbers outside the pool give NaN rows, others stay right."""
+    lens, page = [40, 40, 40, 40], 16
+    table, kc, vc, ks, vs = cache_case(lens, page, 1, 64, "bf16", 79)
+    table[1, 2] = 1 << 30
+    q = torch.randn(4, 2, 64, device="cuda").to(torch.bfloat16)
+    o = decode(q, kc, vc, table, torch.tensor([40, 40, 49, -1], dtype=torch.int32).cuda(), 0.125)
+    assert torch.isnan(o[1:]).all()
+    val, bound = attn_ref.decode(to_f64(q), ks, vs, 0.125, "bf16")
+    within("o", o[:1], (val[:1], bound[:1]))
+
+
+# dtype, new tokens per sequence (None: one each), past, page, Hq, Hkv, hd, rotate
+APPENDS = [
+    ("bf16", None, [0, 1, 15, 16, 100], 16, 4, 2, 64, True),
+    ("bf16", [1, 0, 40, 333], [7, 9, 0, 61], 24, 3, 1, 96, True),
+    ("bf16", [100, 20], [0, 5], 7, 6, 6, 8, False),
+    ("fp32", [5, 130], [1, 1000], 64, 2, 2, 128, True),
+    ("fp32", None, [3], 1, 5, 1, 12, True),
+]
+
+
+@pytest.mark.parametrize("dtype,new,past,page,Hq,Hkv,hd,rotate", APPENDS)
+def test_append(dtype, new, past, page, Hq, Hkv, hd, rotate):
+    say(f"[kv append] {dtype} new={new} past={past} page={page} Hq={Hq} Hkv={Hkv} hd={hd} rotate={rotate}")
+    n = new or [1] * len(past)
+    N, S = sum(n), len(past)
+    table, kc, vc, _, _ = cache_case([a + b for a, b in zip(n, past)], page, Hkv, hd, dtype, 5)
+    kc.fill_(POISON)
+    vc.fill_(POISON)
+    _, q, k, v = qkv(1, N, Hq, Hkv, hd, dtype, 9, pad=8)
+    q, k, v = q[0], k[0], v[0]
+    rope = None
+    if rotate:
+        rope = torch.empty(max(a + b for a, b in zip(n, past)), hd // 2, 2, device="cuda")
+        binding.dsc_rope_table(rope, base=500.0)
+    q_out = torch.full((N, Hq, hd), POISON, dtype=q.dtype, device="cuda")
+    binding.dsc_kv_append(k, v, kc, vc, table, torch.tensor(past, dtype=torch.int32).cuda(), q=q, q_out=q_out,
+                          table=rope, cu_seqlens=None if new is None else cu_of(new))
+    torch.cuda.synchronize()
+    pos = np.concatenate([np.arange(a, a + b) for a, b in zip(past, n)])
+    q64, k64, v64 = to_f64(q), to_f64(k), to_f64(v)
+    if rotate:
+        q64, k64 = attn_ref.rope(q64, pos, 500.0), attn_ref.rope(k64, pos, 500.0)
+    # one rounding of the result (and of cos, sin: 2^-24 each) of a sum of two products
+    u = attn_ref.U[dtype] if rotate else 0.0
+    bound = lambda x: u * np.abs(x) + (1e-6 if rotate else 0.0) * (1 + np.abs(x).max()) + 1e-30
+    within("q", q_out, (q64, bound(q64)))
+    seq, tab = np.repeat(np.arange(S), n), table.cpu().numpy()
+    hk, hv = to_f64(kc), to_f64(vc)
+    pg = tab[seq, pos // page]
+    within("k", hk[pg, :, pos % page], (k64, bound(k64)))
+    within("v", hv[pg, :, pos % page], (v64, np.full_like(v64, 1e-30)))
+    hk[pg, :, pos % page] = POISON
+    hv[pg, :, pos % page] = POISON
+    assert (hk == POISON).all() and (hv == POISON).all(), "places of other tokens were written"
+
+
+def test_append_outside_the_table_or_pool_writes_nothing():
+    kc, vc = (torch.full((3, 1, 4, 8), POISON, device="cuda") for _ in range(2))
+    table = torch.tensor([[0, 1], [2, 99], [-1, 0]], dtype=torch.int32).cuda()
+    k = torch.ones(3, 1, 8, device="cuda")
+    rope = torch.empty(6, 4, 2, device="cuda")
+    binding.dsc_rope_table(rope)
+    q_out = torch.empty(3, 1, 8, device="cuda")
+    binding.dsc_kv_append(k, k, kc, vc, table, torch.tensor([8, 5, 2], dtype=torch.int32).cuda(), q=k, q_out=q_out,
+                          table=rope)
+    torch.cuda.synchronize()
+    assert (kc == POISON).all() and (vc == POISON).all()
+    assert torch.isnan(q_out[0]).all()          # no table row for position 8
+    assert torch.isfinite(q_out[1:]).all()
+
+
+def test_offsets_past_32_bits():
+    """A pool of 5 GiB per side: the pages in use lie past 2^31 elements."""
+    pages, Hkv, page, hd = 20600, 8, 128, 128
+    assert pages * Hkv * page * hd > 2 ** 31
+    kc = torch.zeros(pages, Hkv, page, hd, dtype=torch.bfloat16, device="cuda")
+    vc = torch.zeros_like(kc)
+    table = torch.tensor([[pages - 1, pages - 2]], dtype=torch.int32).cuda()
+    _, q, k, v = qkv(1, 200, 8, Hkv, hd, "bf16", 61)
+    binding.dsc_kv_append(k[0], v[0], kc, vc, table, torch.tensor([0], dtype=torch.int32).cuda(),
+                          cu_seqlens=cu_of([200]))
+    o = decode(q[0, -1:], kc, vc, table, torch.tensor([200], dtype=torch.int32).cuda(), 0.1)
+    within("o", o, attn_ref.decode(to_f64(q[0, -1:]), [to_f64(k[0])], [to_f64(v[0])], float(np.float32(0.1)), "bf16"))
