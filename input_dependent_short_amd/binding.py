@@ -373,57 +373,82 @@ def dsc_state_from_prefill(x, state, *, W, cu_seqlens=None, stream=None) -> None
                                         _ptr(state)))
 
 
-def _rows(t: torch.Tensor, name: str):
-    """Pointer and row stride of token rows (..., heads, head_dim), a view of wider rows or dense."""
-    if t.stride(-1) != 1 or t.stride(-2) != t.shape[-1] and t.shape[-2] > 1:
+# The attention calls are made once per layer and decoding step, where their
+# own cost on the host counts: they read each tensor's sizes once and pass
+# plain integers.
+_CODES = {torch.float32: DSC_FP32, torch.bfloat16: DSC_BF16}
+
+
+def _code(dtype: torch.dtype) -> int:
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return code
+
+
+def _addr(t: torch.Tensor) -> int:
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return t.data_ptr()
+
+
+def _row_stride(t: torch.Tensor, name: str) -> int:
+    """Elements between token rows of t (..., tokens, heads, head_dim), a view of wider rows or dense."""
+    sh, st = t.shape, t.stride()
+    if st[-1] != 1 or st[-2] != sh[-1] and sh[-2] > 1:
         raise ValueError(f"{name}: heads and channels must be contiguous within a token's row")
-    rs = t.stride(-3)
-    if t.shape[-3] == 1:  # a single row per leading index: rows are the leading stride apart
-        rs = t.stride(0) if t.dim() == 4 and t.shape[0] > 1 else t.shape[-2] * t.shape[-1]
-    elif t.dim() == 4 and t.shape[0] > 1 and t.stride(0) != t.shape[1] * rs:
+    if sh[-3] == 1:  # a single row per leading index: rows are the leading stride apart
+        return st[0] if len(sh) == 4 and sh[0] > 1 else sh[-2] * sh[-1]
+    if len(sh) == 4 and sh[0] > 1 and st[0] != sh[1] * st[1]:
         raise ValueError(f"{name}: token rows must be evenly spaced")
-    return ctypes.c_void_p(t.data_ptr()), rs
+    return st[-3]
 
 
-def _same(ref: torch.Tensor, **tensors):
-    """The tensors given have the type and device of ref."""
-    for name, t in tensors.items():
-        if t is not None and (t.dtype != ref.dtype or t.device != ref.device):
-            raise TypeError(f"{name} must be {ref.dtype} on {ref.device}")
+def _like(t: torch.Tensor, ref: torch.Tensor, name: str) -> None:
+    if t.dtype != ref.dtype or t.get_device() != ref.get_device():
+        raise TypeError(f"{name} must be {ref.dtype} on {ref.device}")
 
 
-def _int32(ref: torch.Tensor, **tensors):
-    for name, t in tensors.items():
-        if t is not None and (t.dtype != torch.int32 or t.device != ref.device):
-            raise TypeError(f"{name} must be int32 on {ref.device}")
+def _int32(t: torch.Tensor, ref: torch.Tensor, name: str) -> int:
+    if t.dtype != torch.int32 or t.get_device() != ref.get_device():
+        raise TypeError(f"{name} must be int32 on {ref.device}")
+    return _addr(t)
+
+
+def _queue(stream):
+    """The stream's handle; by default the current device's current one, without making a Stream object."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _attn_shapes(q, k, v):
     if q.dim() != 4 or k.dim() != 4 or k.shape != v.shape or q.shape[:2] != k.shape[:2] or q.shape[3] != k.shape[3]:
         raise ValueError("q must be (B,T,Hq,head_dim), k and v (B,T,Hkv,head_dim)")
-    _same(q, k=k, v=v)
+    _like(k, q, "k")
+    _like(v, q, "v")
 
 
 def _lse(lse, q):
     B, T, Hq, _ = q.shape
-    if lse.dtype != torch.float32 or lse.shape != (Hq, B * T) or lse.device != q.device:
+    if lse.dtype != torch.float32 or lse.shape != (Hq, B * T) or lse.get_device() != q.get_device():
         raise ValueError(f"lse must be fp32 ({Hq}, {B * T}) on {q.device}")
-    return _ptr(lse)
+    return _addr(lse)
 
 
 def dsc_attn_fwd(q, k, v, o, lse=None, *, scale=None, cu_seqlens=None, stream=None) -> None:
     """o (B,T,Hq,hd) <- causal attention of q (B,T,Hq,hd) over k, v (B,T,Hkv,hd), views of [Q | K | V] rows or
     dense; lse (Hq, B*T) fp32 <- the rows' log-sum-exp (optional).  scale defaults to 1/sqrt(hd)."""
     _attn_shapes(q, k, v)
-    _same(q, o=o)
+    _like(o, q, "o")
     if o.shape != q.shape:
         raise ValueError("o must have q's shape")
     B, T, Hq, hd = q.shape
-    (qp, qs), (kp, ks), (vp, vs) = _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
-    _int32(q, cu_seqlens=cu_seqlens)
-    cu, ns = _seq(cu_seqlens)
-    _check(lib().dsc_attn_fwd(_stream(stream), _dtype_code(q), B, T, Hq, k.shape[2], hd, qp, qs, kp, ks, vp, vs, cu,
-                              ns, hd ** -0.5 if scale is None else scale, _ptr(o), None if lse is None else _lse(lse, q)))
+    cu, ns = (None, 0) if cu_seqlens is None else (_int32(cu_seqlens, q, "cu_seqlens"), cu_seqlens.numel() - 1)
+    qs, ks, vs = _row_stride(q, "q"), _row_stride(k, "k"), _row_stride(v, "v")
+    _check(lib().dsc_attn_fwd(_queue(stream), _code(q.dtype), B, T, Hq, k.shape[2], hd,
+                              q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, cu, ns, hd ** -0.5 if scale is None else scale,
+                              _addr(o), None if lse is None else _lse(lse, q)))
 
 
 def dsc_attn_bwd_workspace_size(dtype: torch.dtype, B: int, T: int, Hq: int, Hkv: int, head_dim: int) -> int:
@@ -435,25 +460,28 @@ def dsc_attn_bwd(q, k, v, o, lse, dout, dq, dk, dv, workspace=None, *, scale=Non
                  stream=None) -> None:
     """Gradients dq, dk, dv (like q, k, v; views of one tensor or dense) of dsc_attn_fwd for L = <dout, o>."""
     _attn_shapes(q, k, v)
-    _same(q, o=o, dout=dout, dq=dq, dk=dk, dv=dv)
-    if o.shape != q.shape or dout.shape != q.shape or dq.shape != q.shape or dk.shape != k.shape or dv.shape != k.shape:
-        raise ValueError("o, dout and dq must have q's shape, dk and dv k's")
+    for t, name, like in ((o, "o", q), (dout, "dout", q), (dq, "dq", q), (dk, "dk", k), (dv, "dv", k)):
+        _like(t, q, name)
+        if t.shape != like.shape:
+            raise ValueError(f"{name} must be {tuple(like.shape)}")
     B, T, Hq, hd = q.shape
-    (qp, qs), (kp, ks), (vp, vs) = _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
-    (dqp, dqs), (dkp, dks), (dvp, dvs) = _rows(dq, "dq"), _rows(dk, "dk"), _rows(dv, "dv")
-    _int32(q, cu_seqlens=cu_seqlens)
-    cu, ns = _seq(cu_seqlens)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib().dsc_attn_bwd(_stream(stream), _dtype_code(q), B, T, Hq, k.shape[2], hd, qp, qs, kp, ks, vp, vs,
-                              _ptr(o), _lse(lse, q), _ptr(dout), cu, ns, hd ** -0.5 if scale is None else scale,
-                              dqp, dqs, dkp, dks, dvp, dvs, _ptr(workspace), ws_bytes))
+    cu, ns = (None, 0) if cu_seqlens is None else (_int32(cu_seqlens, q, "cu_seqlens"), cu_seqlens.numel() - 1)
+    ws, ws_bytes = (None, 0) if workspace is None else (_addr(workspace), workspace.numel() * workspace.element_size())
+    qs, ks, vs = _row_stride(q, "q"), _row_stride(k, "k"), _row_stride(v, "v")
+    dqs, dks, dvs = _row_stride(dq, "dq"), _row_stride(dk, "dk"), _row_stride(dv, "dv")
+    _check(lib().dsc_attn_bwd(_queue(stream), _code(q.dtype), B, T, Hq, k.shape[2], hd,
+                              q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, _addr(o), _lse(lse, q), _addr(dout), cu, ns,
+                              hd ** -0.5 if scale is None else scale, dq.data_ptr(), dqs,
+                              dk.data_ptr(), dks, dv.data_ptr(), dvs, ws, ws_bytes))
 
 
 def _cache_shapes(k_cache, v_cache, page_table, S, hd):
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.shape[3] != hd:
+    sh = k_cache.shape
+    if len(sh) != 4 or sh != v_cache.shape or sh[3] != hd:
         raise ValueError(f"k_cache and v_cache must be (num_pages, Hkv, page_size, {hd})")
     if page_table.dim() != 2 or page_table.shape[0] != S:
         raise ValueError(f"page_table must be ({S}, max_pages)")
+    return sh
 
 
 def dsc_kv_append(k, v, k_cache, v_cache, page_table, start, *, q=None, q_out=None, table=None, cu_seqlens=None,
@@ -463,23 +491,33 @@ def dsc_kv_append(k, v, k_cache, v_cache, page_table, start, *, q=None, q_out=No
     cu_seqlens, else the sequences' offsets among the N tokens."""
     N, Hkv, hd = k.shape
     S = start.numel()
-    _cache_shapes(k_cache, v_cache, page_table, S, hd)
-    _same(k, v=v, k_cache=k_cache, v_cache=v_cache, q=q, q_out=q_out)
-    _int32(k, page_table=page_table, start=start, cu_seqlens=cu_seqlens)
-    if v.shape != k.shape or k_cache.shape[1] != Hkv:
+    pages, heads, page, _ = _cache_shapes(k_cache, v_cache, page_table, S, hd)
+    _like(v, k, "v")
+    _like(k_cache, k, "k_cache")
+    _like(v_cache, k, "v_cache")
+    if v.shape != k.shape or heads != Hkv:
         raise ValueError("k, v and the caches must agree in their heads")
-    if cu_seqlens is not None and cu_seqlens.numel() != S + 1:
-        raise ValueError("cu_seqlens must hold one offset more than start")
-    (kp, ks), (vp, vs) = _rows(k, "k"), _rows(v, "v")
+    cu = None
+    if cu_seqlens is not None:
+        cu = _int32(cu_seqlens, k, "cu_seqlens")
+        if cu_seqlens.numel() != S + 1:
+            raise ValueError("cu_seqlens must hold one offset more than start")
     Hq, qp, qs, qop = Hkv, None, 0, None
-    if q is not None:
-        if q_out is None or q_out.shape != q.shape or q.shape[0] != N or q.shape[2] != hd:
-            raise ValueError("q and q_out must be (N, Hq, head_dim)")
-        Hq, (qp, qs), qop = q.shape[1], _rows(q, "q"), _ptr(q_out)
-    tp, max_pos = _table(table, hd)
-    _check(lib().dsc_kv_append(_stream(stream), _dtype_code(k), N, S, Hq, Hkv, hd, qp, qs, kp, ks, vp, vs,
-                               _ptr(cu_seqlens), _ptr(start), tp, max_pos, _ptr(k_cache), _ptr(v_cache),
-                               k_cache.shape[0], k_cache.shape[2], _ptr(page_table), page_table.shape[1], qop))
+    if q is not None or q_out is not None:
+        if q is None or q_out is None or q_out.shape != q.shape or q.dim() != 3 or q.shape[0] != N or q.shape[2] != hd:
+            raise ValueError("q and q_out must both be (N, Hq, head_dim)")
+        _like(q, k, "q")
+        _like(q_out, k, "q_out")
+        Hq, qp, qs, qop = q.shape[1], q.data_ptr(), _row_stride(q, "q"), _addr(q_out)
+    tp, max_pos = None, 0
+    if table is not None:
+        if table.dtype != torch.float32 or table.get_device() != k.get_device() or table.shape[1:] != (hd // 2, 2):
+            raise ValueError(f"table must be fp32 (max_pos, {hd // 2}, 2) on {k.device}")
+        tp, max_pos = _addr(table), table.shape[0]
+    ks, vs, at = _row_stride(k, "k"), _row_stride(v, "v"), _int32(start, k, "start")
+    _check(lib().dsc_kv_append(_queue(stream), _code(k.dtype), N, S, Hq, Hkv, hd, qp, qs,
+                               k.data_ptr(), ks, v.data_ptr(), vs, cu, at, tp, max_pos, _addr(k_cache), _addr(v_cache), pages, page,
+                               _int32(page_table, k, "page_table"), page_table.shape[1], qop))
 
 
 def dsc_attn_decode_workspace_size(dtype: torch.dtype, S: int, Hq: int, Hkv: int, head_dim: int, page_size: int,
@@ -492,17 +530,17 @@ def dsc_attn_decode(q, k_cache, v_cache, page_table, lens, o, workspace=None, *,
     """o (S,Hq,hd) <- attention of one new token per sequence, q (S,Hq,hd), over the first lens[s] tokens of the
     paged cache (num_pages,Hkv,page,hd).  scale defaults to 1/sqrt(hd)."""
     S, Hq, hd = q.shape
-    _cache_shapes(k_cache, v_cache, page_table, S, hd)
-    _same(q, k_cache=k_cache, v_cache=v_cache, o=o)
-    _int32(q, page_table=page_table, lens=lens)
+    pages, Hkv, page, _ = _cache_shapes(k_cache, v_cache, page_table, S, hd)
+    _like(k_cache, q, "k_cache")
+    _like(v_cache, q, "v_cache")
+    _like(o, q, "o")
     if o.shape != q.shape or lens.numel() != S:
         raise ValueError("o must have q's shape, lens one length per sequence")
-    qp, qs = _rows(q, "q")
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib().dsc_attn_decode(_stream(stream), _dtype_code(q), S, Hq, k_cache.shape[1], hd, qp, qs, _ptr(k_cache),
-                                 _ptr(v_cache), k_cache.shape[0], k_cache.shape[2], _ptr(page_table),
-                                 page_table.shape[1], _ptr(lens), hd ** -0.5 if scale is None else scale, _ptr(o),
-                                 _ptr(workspace), ws_bytes))
+    ws, ws_bytes = (None, 0) if workspace is None else (_addr(workspace), workspace.numel() * workspace.element_size())
+    qs, pt, ln = _row_stride(q, "q"), _int32(page_table, q, "page_table"), _int32(lens, q, "lens")
+    _check(lib().dsc_attn_decode(_queue(stream), _code(q.dtype), S, Hq, Hkv, hd, q.data_ptr(), qs, _addr(k_cache),
+                                 _addr(v_cache), pages, page, pt, page_table.shape[1], ln, hd ** -0.5 if scale is None else scale,
+                                 _addr(o), ws, ws_bytes))
 
 
 def dsc_bench_stream(src, read_bytes: int, dst, write_bytes: int, *, unroll=4, load_nt=False, store_nt=False,

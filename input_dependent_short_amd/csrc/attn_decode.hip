@@ -7,13 +7,19 @@
 // decide.  A block takes one (sequence, key head, chunk of the length) and up
 // to 16 query heads of the group (one side of the 16 x 16 matrix
 // instructions); its waves take tiles of kTok tokens in turn, each wave on its
-// own, without barriers: a tile's K and V rows go straight from memory into
-// the wave's own LDS stages, one tile ahead of the one being worked on, with
-// the page numbers looked up one tile earlier still.  Places past the length
-// (and channels past the head's own) are read from a 16-byte zero instead, so
-// what the page holds there never enters.  Scores are formed transposed
-// (S^T = K Q^T), so that the probabilities are the right operand of
-// O^T = V^T P^T without moving between lanes.
+// own, without barriers.  K and V go straight from memory into the registers
+// in which the matrix instructions take them, one tile ahead of the one being
+// worked on, with the page numbers two tiles further ahead: registers hold
+// more of them than LDS would (a form through LDS stages, with half the bytes
+// in flight, read 3.9 TB/s where this one reads 5.5 TB/s).
+//   Scores are formed transposed (S^T = K Q^T): a lane's 16-byte pieces of its
+// token's K row are the left operand as they are.  The probabilities are then
+// the right operand of O^T = V^T P^T without moving between lanes; its left
+// operand wants several tokens of one channel per lane, so a lane loads the
+// same few channels of those tokens and (bf16) pairs them up with byte
+// permutes; product r covers channel r of every lane's piece.
+//   Tokens past the end repeat the last one: their scores are masked, and
+// nothing outside the length is ever read.
 // The waves' results are joined in LDS; when the length is cut into several
 // chunks each writes its maximum, sum and unscaled fp32 row to the workspace
 // and a second launch joins them.
@@ -24,18 +30,17 @@
 namespace dsc {
 namespace {
 
-constexpr int kDecWaves = 2;
+constexpr int kDecWaves = 4;
 
 template <class E>
 constexpr int kTok = sizeof(typename E::store_t) == 2 ? 32 : 16;  // tokens per wave tile
-
-__device__ const uint4 kZeroChunk = {0, 0, 0, 0};
 
 struct DecodeParams {
     const void *q, *k, *v;
     const int32_t *pages, *lens;
     void *o;
-    float *part;  // (S, Hq, nsplit, hd + 2) fp32: row, maximum (base 2), sum
+    float *part;  // (S, Hq, nsplit, hd) fp32: unscaled rows of the chunks
+    float2 *stat;  // (S, Hq, nsplit): maximum (base 2) and sum
     int64_t S, qs, num_pages, max_pages;
     int32_t Hq, Hkv, G, hd, page, page_shift, nsplit, chunk, qtiles;
     float c2;
@@ -72,26 +77,54 @@ __device__ __forceinline__ float groups_sum(float v) {
     return v + __shfl_xor(v, 32);
 }
 
+// A tile's K and V in registers.
 template <class E, int HDC>
-__global__ __launch_bounds__(64 * kDecWaves, 1) void attn_decode_kernel(DecodeParams p) {
-    using T = Tile<E, HDC>;
+struct KvTile {
+    using S = typename E::store_t;
+    using frag = typename Mma16<E>::frag;
+    static constexpr int NS = kTok<E> / 16, KF = HDC / Mma16<E>::KC;
+    static constexpr int NV = kTok<E> / 4;                                 // tokens per lane of V
+    static constexpr int PC = HDC / 16 < E::kVec ? HDC / 16 : E::kVec;     // channels per V piece
+    static constexpr int NP = HDC / 16 / PC;                               // pieces: channels 16*PC*c + PC*(lane%16) ..
+    static constexpr int PW = PC * (int)sizeof(S) / 4;                     // 32-bit words per piece
+    frag k[NS][KF];
+    uint32_t v[NV][NP][PW];
+};
+
+template <int W>
+__device__ __forceinline__ void load_words(uint32_t (&w)[W], const void *p) {
+    if constexpr (W == 4) {
+        const uint4 q = *static_cast<const uint4 *>(p);
+        w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+    } else {
+        static_assert(W == 2, "piece size");
+        const uint2 q = *static_cast<const uint2 *>(p);
+        w[0] = q.x, w[1] = q.y;
+    }
+}
+
+template <class E, int HDC>
+__global__ __launch_bounds__(64 * kDecWaves, 2) void attn_decode_kernel(DecodeParams p) {
     using M = Mma16<E>;
     using S = typename E::store_t;
     using frag = typename M::frag;
-    constexpr int TN = kTok<E>, NS = TN / 16, KF = HDC / M::KC, DT = HDC / 16, NW = kDecWaves;
-    constexpr int TB = TN * T::RB;               // bytes of a K (or V) tile
-    constexpr int INST = TB / 1024, RPI = 1024 / T::RB;  // load instructions per tile, rows per instruction
-    __shared__ __align__(16) unsigned char k0s[NW][TB], v0s[NW][TB], k1s[NW][TB], v1s[NW][TB];
+    using KV = KvTile<E, HDC>;
+    constexpr int TN = kTok<E>, NS = KV::NS, KF = KV::KF, DT = HDC / 16, NW = kDecWaves, VEC = E::kVec;
+    __shared__ float rows[NW][HDC][16];  // the waves' unscaled rows, channel by column
+    __shared__ float2 stat[NW][16];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 15, grp = lane >> 4;
     int64_t b = blockIdx.x;
-    const int split = (int)(b % p.nsplit);
-    b /= p.nsplit;
+    // Chunk slowest: blocks b, b + 8, ... share an XCD, and the later chunks of
+    // ragged sequences are mostly empty, so with the chunk fastest some XCDs
+    // would get most of the work.
     const int qt = (int)(b % p.qtiles);
     b /= p.qtiles;
     const int kvh = (int)(b % p.Hkv);
-    const int64_t seq = b / p.Hkv;
+    b /= p.Hkv;
+    const int64_t seq = b % p.S;
+    const int split = (int)(b / p.S);
     const int64_t cap = p.max_pages * p.page;
     int len = p.lens[seq];
     bool bad = len < 0 || len > cap;
@@ -101,76 +134,86 @@ __global__ __launch_bounds__(64 * kDecWaves, 1) void attn_decode_kernel(DecodePa
 
     // queries: column col is head qt*16 + col of the group
     const int a = qt * 16 + col;
-    const bool live = a < p.G;
     const int64_t head = (int64_t)kvh * p.G + a;
     frag qf[KF];
 #pragma unroll
     for (int kc = 0; kc < KF; ++kc) {
-        const int d = T::VEC * (4 * kc + grp);
+        const int d = VEC * (4 * kc + grp);
         uint4 v = make_uint4(0, 0, 0, 0);
-        if (live && d < p.hd) v = *reinterpret_cast<const uint4 *>(static_cast<const S *>(p.q) + seq * p.qs + head * p.hd + d);
+        if (a < p.G && d < p.hd)
+            v = *reinterpret_cast<const uint4 *>(static_cast<const S *>(p.q) + seq * p.qs + head * p.hd + d);
         qf[kc] = __builtin_bit_cast(frag, v);
     }
 
     const int32_t *pages = p.pages + seq * p.max_pages;
-    // Page number of this lane's token of the tile at t0 (tokens past the end
-    // repeat the last one's: the load is never skipped, so that the loads in
-    // flight can be counted).
+    const int t_last = max(t_hi - 1, 0);
     auto page_of = [&](int t) __attribute__((always_inline)) {
         return p.page_shift >= 0 ? (uint32_t)t >> p.page_shift : (uint32_t)t / (uint32_t)p.page;
     };
-    const int t_last = max(t_hi - 1, 0);
+    // Page number of token t0 + lane % TN (of the last token past the end).
     auto lookup = [&](int t0) __attribute__((always_inline)) -> int32_t {
         return pages[page_of(min(t0 + (lane & (TN - 1)), t_last))];
     };
-    // K and V rows of the tile at t0, whose lanes looked up pg.  A page number
-    // outside the pool spoils the result.
-    auto issue = [&](int t0, int32_t pg, unsigned char *ks, unsigned char *vs) __attribute__((always_inline)) {
-        const int t = t0 + (lane & (TN - 1));
+    // K and V of the tile at t0, whose lanes looked up pg.  A page number
+    // outside the pool spoils the result and reads page 0.
+    auto load = [&](KV &x, int t0, int32_t pg) __attribute__((always_inline)) {
+        const int t = min(t0 + (lane & (TN - 1)), t_last);
         const bool in_pool = pg >= 0 && pg < p.num_pages;
-        bad |= t < t_hi && !in_pool;
-        const int64_t slot = t < t_hi && in_pool
-                                 ? ((int64_t)pg * p.Hkv + kvh) * p.page + (t - (int)page_of(t) * p.page)
-                                 : -1;
+        bad |= !in_pool;
+        const int64_t row = (((int64_t)(in_pool ? pg : 0) * p.Hkv + kvh) * p.page + (t - (int)page_of(t) * p.page)) * p.hd;
 #pragma unroll
-        for (int i = 0; i < INST; ++i) {
-            const int row = i * RPI + lane / T::NCH, c = (lane % T::NCH) ^ T::swz(row);
-            const int64_t r = __shfl(slot, row);
-            const bool in = r >= 0 && c * T::VEC < p.hd;
-            const int64_t off = r * p.hd + c * T::VEC;
-            const void *kp = in ? (const void *)(static_cast<const S *>(p.k) + off) : (const void *)&kZeroChunk;
-            const void *vp = in ? (const void *)(static_cast<const S *>(p.v) + off) : (const void *)&kZeroChunk;
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)kp,
-                                             (attn_lds_void *)(ks + 1024 * i), 16, 0, 0);
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)vp,
-                                             (attn_lds_void *)(vs + 1024 * i), 16, 0, 0);
+        for (int j = 0; j < NS; ++j) {
+            const S *r = static_cast<const S *>(p.k) + __shfl(row, 16 * j + col);
+#pragma unroll
+            for (int kc = 0; kc < KF; ++kc) {
+                const int d = VEC * (4 * kc + grp);
+                x.k[j][kc] = __builtin_bit_cast(frag, *reinterpret_cast<const uint4 *>(r + (d < p.hd ? d : 0)));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < KV::NV; ++i) {
+            const S *r = static_cast<const S *>(p.v) + __shfl(row, 16 * (i / 4) + 4 * grp + i % 4);
+#pragma unroll
+            for (int c = 0; c < KV::NP; ++c) {
+                const int d = 16 * KV::PC * c + KV::PC * col;
+                load_words(x.v[i][c], r + (d < p.hd ? d : 0));
+            }
         }
     };
 
-    floatx4 acc[DT];
+    floatx4 acc[DT];  // product r of piece c: acc[c*PC + r][i] = channel 16*PC*c + PC*(4 grp + i) + r, column col
 #pragma unroll
     for (int d = 0; d < DT; ++d) acc[d] = floatx4{0.f, 0.f, 0.f, 0.f};
     float mx = -INFINITY, sum = 0.f;
+    const bool pad = p.hd < HDC;
 
-    auto compute = [&](int t0, const unsigned char *ks, const unsigned char *vs) __attribute__((always_inline)) {
+    auto compute = [&](KV &x, int t0) __attribute__((always_inline)) {
+        if (pad) {  // channels past the head's own: q is zero there, and so must K be, whatever was read
+#pragma unroll
+            for (int kc = 0; kc < KF; ++kc)
+                if (VEC * (4 * kc + grp) >= p.hd)
+#pragma unroll
+                    for (int j = 0; j < NS; ++j) x.k[j][kc] = __builtin_bit_cast(frag, make_uint4(0, 0, 0, 0));
+        }
         floatx4 s[NS];
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
             s[j] = floatx4{0.f, 0.f, 0.f, 0.f};
-            const int r = 16 * j + col;
 #pragma unroll
-            for (int kc = 0; kc < KF; ++kc)
-                s[j] = M::mul(*reinterpret_cast<const frag *>(ks + r * T::RB + 16 * ((4 * kc + grp) ^ T::swz(r))),
-                              qf[kc], s[j]);
+            for (int kc = 0; kc < KF; ++kc) s[j] = M::mul(x.k[j][kc], qf[kc], s[j]);
         }
         float top = -INFINITY;
+        if (t0 + TN > t_hi) {
+#pragma unroll
+            for (int j = 0; j < NS; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (t0 + 16 * j + 4 * grp + i >= t_hi) s[j][i] = -INFINITY;
+        }
 #pragma unroll
         for (int j = 0; j < NS; ++j)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (t0 + 16 * j + 4 * grp + i >= t_hi) s[j][i] = -INFINITY;
-                top = fmaxf(top, s[j][i]);
-            }
+            for (int i = 0; i < 4; ++i) top = fmaxf(top, s[j][i]);
         top = groups_max(top);
         const float nm = fmaxf(mx, top), safe = nm == -INFINITY ? 0.f : nm;
         const float al = __builtin_amdgcn_exp2f((mx - safe) * p.c2);
@@ -185,85 +228,79 @@ __global__ __launch_bounds__(64 * kDecWaves, 1) void attn_decode_kernel(DecodePa
                 s[j][i] = __builtin_amdgcn_exp2f((s[j][i] - safe) * p.c2);
                 sum += s[j][i];
             }
-        frag pf;
-        if constexpr (sizeof(S) == 2)
-            pf = __builtin_bit_cast(frag, make_uint4(pack_bf16x2(s[0][0], s[0][1]), pack_bf16x2(s[0][2], s[0][3]),
-                                                     pack_bf16x2(s[1][0], s[1][1]), pack_bf16x2(s[1][2], s[1][3])));
-        else
-            pf = s[0];
+        if constexpr (sizeof(S) == 2) {
+            const frag pf = __builtin_bit_cast(frag, make_uint4(pack_bf16x2(s[0][0], s[0][1]), pack_bf16x2(s[0][2], s[0][3]),
+                                                                pack_bf16x2(s[1][0], s[1][1]), pack_bf16x2(s[1][2], s[1][3])));
 #pragma unroll
-        for (int d = 0; d < DT; ++d) {
-            frag vf;
-            if constexpr (sizeof(S) == 2) {
-                // a 16-lane group reads a 4 x 16 block (rows 4 grp + 0..3), lane i its 8-byte piece i, and gets column i
-                const int r = 4 * grp + (col >> 2), c = 2 * d + ((col >> 1) & 1);
-                const shortx4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (attn_lds_s4 *)(vs + r * T::RB + 16 * (c ^ T::swz(r)) + 8 * (col & 1)));
-                const shortx4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (attn_lds_s4 *)(vs + (r + 16) * T::RB + 16 * (c ^ T::swz(r + 16)) + 8 * (col & 1)));
-                vf = __builtin_bit_cast(frag, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
-            } else {
-                const int ch = 16 * d + col;
+            for (int c = 0; c < KV::NP; ++c)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = 4 * grp + i;
-                    vf[i] = *reinterpret_cast<const float *>(vs + r * T::RB + 16 * ((ch >> 2) ^ T::swz(r)) + 4 * (ch & 3));
+                for (int r = 0; r < KV::PC; ++r) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)  // low (even r) or high halves of two tokens' words
+                        w[i] = __builtin_amdgcn_perm(x.v[2 * i + 1][c][r / 2], x.v[2 * i][c][r / 2],
+                                                     r % 2 ? 0x07060302u : 0x05040100u);
+                    acc[c * KV::PC + r] = M::mul(__builtin_bit_cast(frag, make_uint4(w[0], w[1], w[2], w[3])), pf,
+                                                 acc[c * KV::PC + r]);
                 }
-            }
-            acc[d] = M::mul(vf, pf, acc[d]);
+        } else {
+#pragma unroll
+            for (int c = 0; c < KV::NP; ++c)
+#pragma unroll
+                for (int r = 0; r < KV::PC; ++r) {
+                    frag vf;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) vf[i] = __uint_as_float(x.v[i][c][r]);
+                    acc[c * KV::PC + r] = M::mul(vf, s[0], acc[c * KV::PC + r]);
+                }
         }
     };
 
-    // Tile i of the wave: tokens t_lo + (i*NW + wave)*TN.  While it is worked
-    // on, the loads of tile i+1 (2*INST instructions) and, behind them, of the
-    // page numbers of tile i+3 are in flight.
+    // Tile i of the wave: tokens t_lo + (i*NW + wave)*TN.
     constexpr int STEP = NW * TN;
     const int tw = t_lo + wave * TN;
-    const int32_t pg0 = lookup(tw);
-    int32_t pg1 = lookup(tw + STEP), pg2 = 0;
-    issue(tw, pg0, k0s[wave], v0s[wave]);
-    pg2 = lookup(tw + 2 * STEP);
-    auto step = [&](int t0, int32_t &pg, unsigned char *ks, unsigned char *vs, unsigned char *kn,
-                    unsigned char *vn) __attribute__((always_inline)) {
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the stage refilled below has been read
-        issue(t0 + STEP, pg, kn, vn);
-        pg = lookup(t0 + 3 * STEP);
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * INST + 1) : "memory");
-        compute(t0, ks, vs);
-    };
-    for (int t0 = tw; t0 < t_hi; t0 += 2 * STEP) {
-        step(t0, pg1, k0s[wave], v0s[wave], k1s[wave], v1s[wave]);
-        if (t0 + STEP < t_hi) step(t0 + STEP, pg2, k1s[wave], v1s[wave], k0s[wave], v0s[wave]);
+    if (tw < t_hi) {
+        KV x0, x1;
+        int32_t pg = lookup(tw), pg1 = lookup(tw + STEP);
+        load(x0, tw, pg);
+        int32_t pg2 = lookup(tw + 2 * STEP);
+        for (int t0 = tw;; t0 += 2 * STEP) {
+            load(x1, t0 + STEP, pg1);
+            pg1 = lookup(t0 + 3 * STEP);
+            compute(x0, t0);
+            if (t0 + STEP >= t_hi) break;
+            load(x0, t0 + 2 * STEP, pg2);
+            pg2 = lookup(t0 + 4 * STEP);
+            compute(x1, t0 + STEP);
+            if (t0 + 2 * STEP >= t_hi) break;
+        }
     }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     sum = groups_sum(sum);
     if (__any(bad)) sum = __builtin_nanf("");
 
-    // Join of the two waves over the stages: rows (HDC, 16) of each, then (2, 16) maximum and sum.
-    static_assert(NW == 2 && NW * TB >= 16 * HDC * 4, "the join takes two waves whose rows fit a stage array each");
-    __syncthreads();
-    float *r0 = reinterpret_cast<float *>(&k0s[0][0]), *r1 = reinterpret_cast<float *>(&v0s[0][0]);
-    float *st = reinterpret_cast<float *>(&k1s[0][0]);
 #pragma unroll
-    for (int d = 0; d < DT; ++d)
+    for (int c = 0; c < KV::NP; ++c)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int ch = 16 * d + 4 * grp + i;
-            (wave == 0 ? r0 : r1)[ch * 16 + col] = acc[d][i];
-        }
-    if (grp == 0) {
-        st[(wave * 16 + col) * 2] = mx;
-        st[(wave * 16 + col) * 2 + 1] = sum;
-    }
+        for (int r = 0; r < KV::PC; ++r)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                rows[wave][16 * KV::PC * c + KV::PC * (4 * grp + i) + r][col] = acc[c * KV::PC + r][i];
+    if (grp == 0) stat[wave][col] = make_float2(mx, sum);
     __syncthreads();
     for (int e = tid; e < 16 * p.hd; e += 64 * NW) {
         const int c = e / p.hd, d = e - c * p.hd;
         if (qt * 16 + c >= p.G) break;
-        const float m0 = st[c * 2], m1 = st[(16 + c) * 2];
-        const float m = fmaxf(m0, m1), safe = m == -INFINITY ? 0.f : m;
-        const float w0 = __builtin_amdgcn_exp2f((m0 - safe) * p.c2), w1 = __builtin_amdgcn_exp2f((m1 - safe) * p.c2);
-        const float l = st[c * 2 + 1] * w0 + st[(16 + c) * 2 + 1] * w1;
-        const float r = r0[d * 16 + c] * w0 + r1[d * 16 + c] * w1;
+        float m = stat[0][c].x;
+#pragma unroll
+        for (int w = 1; w < NW; ++w) m = fmaxf(m, stat[w][c].x);
+        const float safe = m == -INFINITY ? 0.f : m;
+        float l = 0.f, r = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            const float e2 = __builtin_amdgcn_exp2f((stat[w][c].x - safe) * p.c2);
+            l = __builtin_fmaf(stat[w][c].y, e2, l);
+            r = __builtin_fmaf(rows[w][d][c], e2, r);
+        }
         const int64_t hq = (int64_t)kvh * p.G + qt * 16 + c;
         if (p.nsplit == 1) {
             const float out = r * (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l));
@@ -271,71 +308,106 @@ __global__ __launch_bounds__(64 * kDecWaves, 1) void attn_decode_kernel(DecodePa
             if constexpr (sizeof(S) == 4) *dst = out;
             else *dst = to_bf16(out);
         } else {
-            float *dst = p.part + ((seq * p.Hq + hq) * p.nsplit + split) * (p.hd + 2);
-            dst[d] = r;
-            if (d == 0) {
-                dst[p.hd] = m * p.c2;
-                dst[p.hd + 1] = l;
-            }
+            const int64_t at = (seq * p.Hq + hq) * p.nsplit + split;
+            p.part[at * p.hd + d] = r;
+            if (d == 0) p.stat[at] = make_float2(m * p.c2, l);
         }
     }
 }
 
-// Chunks of one (sequence, query head) joined; one wave each.
+// Chunks of one (sequence, query head) joined by one block: the chunks'
+// weights 2^(m_i - max) / sum into LDS, then four channels per thread and
+// every (256 / threads per row)-th chunk, added up over LDS in a fixed order.
+// Chunk sizes and counts, see plan().
+constexpr int64_t kUnit = 32 * kDecWaves, kFew = 256, kLong = 1024, kMany = 4096;
+constexpr int kMaxSplit = kMany + 1;  // chunk >= floor(cap / kMany)
+
 template <class E>
-__global__ __launch_bounds__(64) void attn_decode_join(DecodeParams p) {
+__global__ __launch_bounds__(256) void attn_decode_join(DecodeParams p) {
     using S = typename E::store_t;
+    __shared__ float w[kMaxSplit];
+    __shared__ float red[4], redl[4];
+    __shared__ float4 rows[256];
     const int64_t row = blockIdx.x;
     const int64_t seq = row / p.Hq, cap = p.max_pages * p.page;
+    const int tid = threadIdx.x, wave = tid >> 6;
     int len = p.lens[seq];
     if (len < 0 || len > cap) len = 0;
     const int n = len > 0 ? (len + p.chunk - 1) / p.chunk : 1;
-    const float *src = p.part + row * p.nsplit * (p.hd + 2);
-    const int lane = threadIdx.x;
+    const float2 *stat = p.stat + row * p.nsplit;
     float m = -INFINITY;
-    for (int i = lane; i < n; i += 64) m = fmaxf(m, src[(int64_t)i * (p.hd + 2) + p.hd]);
+    for (int i = tid; i < n; i += 256) m = fmaxf(m, stat[i].x);
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
-    const float safe = m == -INFINITY ? 0.f : m;
+    if ((tid & 63) == 0) red[wave] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    if (m == -INFINITY) m = 0.f;
     float l = 0.f;
-    for (int i = 0; i < n; ++i) {
-        const float *r = src + (int64_t)i * (p.hd + 2);
-        l += r[p.hd + 1] * __builtin_amdgcn_exp2f(r[p.hd] - safe);
+    for (int i = tid; i < n; i += 256) {
+        const float2 st = stat[i];
+        const float e = __builtin_amdgcn_exp2f(st.x - m);
+        w[i] = e;
+        l = __builtin_fmaf(st.y, e, l);
     }
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-    for (int d = lane; d < p.hd; d += 64) {
-        float a = 0.f;
-        for (int i = 0; i < n; ++i) {
-            const float *r = src + (int64_t)i * (p.hd + 2);
-            a = __builtin_fmaf(r[d], __builtin_amdgcn_exp2f(r[p.hd] - safe), a);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) l += __shfl_xor(l, d);
+    if ((tid & 63) == 0) redl[wave] = l;
+    __syncthreads();
+    l = (redl[0] + redl[1]) + (redl[2] + redl[3]);
+    const int tpr = p.hd / 4, ng = 256 / tpr, g = tid / tpr, c = 4 * (tid - g * tpr);
+    const float *src = p.part + row * p.nsplit * p.hd + c;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (g < ng) {
+#pragma unroll 4
+        for (int i = g; i < n; i += ng) {
+            const float4 v = *reinterpret_cast<const float4 *>(src + (int64_t)i * p.hd);
+            const float e = w[i];
+            a.x = __builtin_fmaf(v.x, e, a.x), a.y = __builtin_fmaf(v.y, e, a.y);
+            a.z = __builtin_fmaf(v.z, e, a.z), a.w = __builtin_fmaf(v.w, e, a.w);
         }
-        S *dst = static_cast<S *>(p.o) + row * p.hd + d;
-        if constexpr (sizeof(S) == 4) *dst = a * inv;
-        else *dst = to_bf16(a * inv);
+    }
+    rows[tid] = a;
+    __syncthreads();
+    if (tid < tpr) {
+        for (int i = 1; i < ng; ++i) {
+            const float4 v = rows[i * tpr + tid];
+            a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
+        }
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+        S *dst = static_cast<S *>(p.o) + row * p.hd + c;
+        if constexpr (sizeof(S) == 4)
+            *reinterpret_cast<float4 *>(dst) = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+        else
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
     }
 }
 
-// Tokens per block and blocks per row: chunks of a multiple of kUnit tokens,
-// as long as about kTarget blocks remain over the longest length the page
-// table can hold.
-constexpr int64_t kUnit = 128, kTarget = 2048;
+// Tokens per block, a multiple of kUnit (one tile per wave).  Work is what the
+// page table can hold, rows * cap tokens.  While that leaves the device with
+// fewer than kFew blocks, a block's time is a chain of tiles, and the shortest
+// chunk is best (one sequence of 12 heads over 777 tokens: 8.5 us in chunks of
+// 128, 10.0 us in one; 8 heads over 4000 tokens: 9.8 against 16.7 us in chunks
+// of 1024).  From there blocks grow to kLong tokens, which covers their start
+// (2 sequences of up to 131073 tokens, 4 key head rows, fp32: 99 us in chunks
+// of 1024, 105 in 512), and beyond kMany blocks they grow again (64 sequences
+// of up to 16384 tokens, 512 rows: 342 us with 4096 blocks, 354 with 2048).
 void plan(int64_t S, int32_t Hq, int32_t Hkv, int32_t page, int64_t max_pages, int32_t &chunk, int32_t &nsplit,
           int32_t &qtiles) {
     const int32_t G = Hq / Hkv;
     qtiles = (G + 15) / 16;
     const int64_t cap = std::max<int64_t>(1, page * max_pages), rows = std::max<int64_t>(1, S * Hkv * qtiles);
-    const int64_t per = std::max<int64_t>(1, kTarget / rows);  // chunks per row
-    const int64_t c = ((cap + per - 1) / per + kUnit - 1) / kUnit * kUnit;
-    chunk = (int32_t)std::min<int64_t>(c, (int64_t)1 << 30);
+    const int64_t work = rows * cap;  // below 2^50: rows < 2^20, cap <= 2^30
+    const int64_t c = std::max(std::min(kLong, work / kFew), work / kMany);
+    chunk = (int32_t)std::min<int64_t>(std::max<int64_t>(1, (c + kUnit - 1) / kUnit) * kUnit, (int64_t)1 << 30);
     nsplit = (int32_t)((cap + chunk - 1) / chunk);
 }
-
 template <class E>
 void run(DecodeParams &p, hipStream_t s) {
     const dim3 grid((unsigned)(p.S * p.Hkv * p.qtiles * p.nsplit)), block(64 * kDecWaves);
     if (p.hd <= 64) hipLaunchKernelGGL((attn_decode_kernel<E, 64>), grid, block, 0, s, p);
     else hipLaunchKernelGGL((attn_decode_kernel<E, 128>), grid, block, 0, s, p);
-    if (p.nsplit > 1) hipLaunchKernelGGL((attn_decode_join<E>), dim3((unsigned)(p.S * p.Hq)), dim3(64), 0, s, p);
+    if (p.nsplit > 1) hipLaunchKernelGGL((attn_decode_join<E>), dim3((unsigned)(p.S * p.Hq)), dim3(256), 0, s, p);
 }
 
 }  // namespace
@@ -347,9 +419,10 @@ size_t attn_decode_workspace(int64_t S, int32_t Hq, int32_t Hkv, int32_t hd, int
 }
 
 hipError_t attn_decode(const AttnDecodeProblem &a, hipStream_t s) {
-    DecodeParams p{a.q, a.c.k, a.c.v, a.c.pages, a.lens, a.o, static_cast<float *>(a.ws), a.S, a.qs, a.c.num_pages,
+    DecodeParams p{a.q, a.c.k, a.c.v, a.c.pages, a.lens, a.o, static_cast<float *>(a.ws), nullptr, a.S, a.qs, a.c.num_pages,
                    a.c.max_pages, a.Hq, a.c.Hkv, a.Hq / a.c.Hkv, a.c.hd, a.c.page, -1, 1, 1, 1, a.scale * kLog2e};
     plan(a.S, a.Hq, a.c.Hkv, a.c.page, a.c.max_pages, p.chunk, p.nsplit, p.qtiles);
+    p.stat = reinterpret_cast<float2 *>(p.part + a.S * a.Hq * p.nsplit * a.c.hd);  // hd is a multiple of 4: aligned
     if ((a.c.page & (a.c.page - 1)) == 0) p.page_shift = __builtin_ctz((unsigned)a.c.page);
     if (a.dtype == Dtype::BF16) run<BF16>(p, s);
     else run<F32>(p, s);

@@ -900,7 +900,8 @@ dsc_status dsc_attn_decode(void *stream, int dtype, int64_t S, int32_t Hq, int32
     DSC_TRY(check_stride("q", dtype, q_stride, Hq, head_dim));
     if (S == 0) return ok();
     if (!q || !page_table || !lens || !o) return fail(DSC_ERR_NULL, "q, page_table, lens and o are required");
-    if (num_pages > 0 && (!k_cache || !v_cache)) return fail(DSC_ERR_NULL, "k_cache and v_cache are required");
+    if (num_pages < 1) return fail(DSC_ERR_SHAPE, "num_pages = %lld: the pool is empty", (long long)num_pages);
+    if (!k_cache || !v_cache) return fail(DSC_ERR_NULL, "k_cache and v_cache are required");
     if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o) || !aligned16(workspace))
         return fail(DSC_ERR_ALIGNMENT, "pointers must be 16-byte aligned");
     if (((uintptr_t)page_table | (uintptr_t)lens) & 3u)
