@@ -30,6 +30,7 @@ FLAGS = [
 # kernels keep the compiler's default register form.
 FILE_FLAGS = {
     "lowrank_fwd.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+    "attn_bwd.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
 }
 
 

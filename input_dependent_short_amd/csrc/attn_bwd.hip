@@ -28,10 +28,12 @@ struct BwdParams {
     int32_t Hq, Hkv, G, hd;
     float scale, c2;
     int64_t ntiles;
+    bool order;  // heaviest tiles first
 };
 
 template <class E>
 constexpr int kBT = sizeof(typename E::store_t) == 2 ? 64 : 32;  // rows per walked tile
+
 
 template <class E, int HDC>
 __global__ __launch_bounds__(256, sizeof(typename E::store_t) == 2 ? 2 : 1) void attn_dq_kernel(BwdParams p) {
@@ -40,16 +42,13 @@ __global__ __launch_bounds__(256, sizeof(typename E::store_t) == 2 ? 2 : 1) void
     using S = typename E::store_t;
     using frag = typename M::frag;
     constexpr int BN = kBT<E>, BM = 128, NS = BN / 32, KF = HDC / M::KC, DT = HDC / 32, PF = 16 / M::PR;
-    __shared__ __align__(16) unsigned char k0s[BN * T::RB], v0s[BN * T::RB], k1s[BN * T::RB], v1s[BN * T::RB];
+    __shared__ __align__(512) unsigned char k0s[BN * T::RB], v0s[BN * T::RB], k1s[BN * T::RB], v1s[BN * T::RB];
     __shared__ int flag;
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
-    const int64_t lb = xcd_block_id(blockIdx.x, (int64_t)gridDim.x);
-    const int g = (int)(lb % p.G);
-    const int64_t rest = lb / p.G;
-    const int kvh = (int)(rest / p.ntiles);
-    const int64_t tile = p.ntiles - 1 - rest % p.ntiles;
-    const int qh = kvh * p.G + g;
+    const typename T::Lane lofs(lane);
+    const int head = (int)(blockIdx.x % p.Hq), kvh = head % p.Hkv, qh = kvh * p.G + head / p.Hkv;
+    const int64_t tile = heavy_tile<false>(p.seq, p.N, p.ntiles, blockIdx.x / p.Hq, p.order, reinterpret_cast<int *>(k0s), tid);
     const int64_t m0 = tile * BM, w0 = m0 + 32 * wave, row = w0 + (lane & 31);
 
     int64_t start, blk_start, end;
@@ -96,16 +95,15 @@ __global__ __launch_bounds__(256, sizeof(typename E::store_t) == 2 ? 2 : 1) void
 #pragma unroll
     for (int d = 0; d < DT; ++d) acc[d] = zero16();
 
-    auto compute = [&](int n0, bool dirty, const unsigned char *ks, const unsigned char *vs) __attribute__((always_inline)) {
-        if (n0 > wlast || n0 + BN <= wfirst_key) return;
-        const bool masked = n0 + BN - 1 > (int)w0 || n0 < wlast_start;
+    auto compute = [&](bool masked, int n0, bool dirty, const unsigned char *ks, const unsigned char *vs) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
+            const typename T::Lane ln = lofs.fresh();
             floatx16 s = zero16(), dp = zero16();
 #pragma unroll
-            for (int kc = 0; kc < KF; ++kc) s = M::mul(T::read_row(ks, 32 * j, kc, lane), qf[kc], s);
+            for (int kc = 0; kc < KF; ++kc) s = M::mul(T::read_row(ks, 32 * j, kc, ln), qf[kc], s);
 #pragma unroll
-            for (int kc = 0; kc < KF; ++kc) dp = M::mul(T::read_row(vs, 32 * j, kc, lane), gf[kc], dp);
+            for (int kc = 0; kc < KF; ++kc) dp = M::mul(T::read_row(vs, 32 * j, kc, ln), gf[kc], dp);
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], p.c2, -lse2)) * (dp[i] - delta);
@@ -123,7 +121,7 @@ __global__ __launch_bounds__(256, sizeof(typename E::store_t) == 2 ? 2 : 1) void
                     const frag df = M::pack(s, f);
 #pragma unroll
                     for (int d = 0; d < DT; ++d)
-                        acc[d] = M::mul(T::finite(T::read_tr(ks, 32 * j, f, d, lane)), df, acc[d]);
+                        acc[d] = M::mul(T::finite(T::read_tr(ks, 32 * j, f, d, ln)), df, acc[d]);
                 }
                 continue;
             }
@@ -131,7 +129,7 @@ __global__ __launch_bounds__(256, sizeof(typename E::store_t) == 2 ? 2 : 1) void
             for (int f = 0; f < PF; ++f) {
                 const frag df = M::pack(s, f);
 #pragma unroll
-                for (int d = 0; d < DT; ++d) acc[d] = M::mul(T::read_tr(ks, 32 * j, f, d, lane), df, acc[d]);
+                for (int d = 0; d < DT; ++d) acc[d] = M::mul(T::read_tr(ks, 32 * j, f, d, ln), df, acc[d]);
             }
         }
     };
@@ -143,7 +141,8 @@ __global__ __launch_bounds__(256, sizeof(typename E::store_t) == 2 ? 2 : 1) void
         issue(n0 + BN, kn, vn);
         const bool dirty = (n0 + BN - 1 > (int)m0 || n0 < blk_last_start) &&
                            tile_dirty<T, BN, 4, false>(ks, nullptr, &flag, n0, wave, lane);
-        compute(n0, dirty, ks, vs);
+        if (n0 > wlast || n0 + BN <= wfirst_key) return;  // no key of the tile is seen by the wave
+        compute(n0 + BN - 1 > (int)w0 || n0 < wlast_start, n0, dirty, ks, vs);
     };
     issue(kv0, k0s, v0s);
     for (int n0 = kv0; n0 < kv_end; n0 += 2 * BN) {
@@ -153,21 +152,43 @@ __global__ __launch_bounds__(256, sizeof(typename E::store_t) == 2 ? 2 : 1) void
     T::store_row(acc, p.scale, static_cast<S *>(p.dq) + (int64_t)qh * p.hd, p.dqs, row, p.N, p.hd, lane);
 }
 
+// Two waves per SIMD hide each other's exponentials and LDS latency, as long
+// as nothing spills (spilled forms ran two to four times longer).  bf16 heads
+// over 64 channels get there (256 registers) with V in LDS, 32 query rows per
+// step and the phases of a step kept apart from the scheduler, which would
+// pull fragment reads forward (packed ~2B shape: 817 us; 64 keys per wave on
+// one wave per SIMD, which halves the LDS reads per product, 1300 us; K and V
+// in registers on one wave per SIMD 910 us).  Smaller heads have registers to
+// spare: K and V in registers, 64 rows per step (~150M shape: 180 us against
+// 220 us the other way).
 template <class E, int HDC>
-__global__ __launch_bounds__(256, sizeof(typename E::store_t) == 2 ? 2 : 1) void attn_dkv_kernel(BwdParams p) {
+struct DkvCfg {
+    static constexpr bool kBig = sizeof(typename E::store_t) == 2 && HDC > 64;
+    static constexpr int NW = 4, BQ = sizeof(typename E::store_t) == 2 && !kBig ? 64 : 32;
+    static constexpr int kOcc = sizeof(typename E::store_t) == 2 ? 2 : 1;
+};
+
+template <class E, int HDC>
+__global__ __launch_bounds__((64 * DkvCfg<E, HDC>::NW), (DkvCfg<E, HDC>::kOcc)) void attn_dkv_kernel(BwdParams p) {
+    using C = DkvCfg<E, HDC>;
+    constexpr int NW = C::NW;
+    constexpr bool VL = C::kBig;
     using T = Tile<E, HDC>;
     using M = Mma<E>;
     using S = typename E::store_t;
     using frag = typename M::frag;
-    constexpr int BQ = kBT<E>, BK = 128, NS = BQ / 32, KF = HDC / M::KC, DT = HDC / 32, PF = 16 / M::PR;
-    __shared__ __align__(16) unsigned char q0s[BQ * T::RB], g0s[BQ * T::RB], q1s[BQ * T::RB], g1s[BQ * T::RB];
+    constexpr int BQ = C::BQ, BK = 32 * NW, NS = BQ / 32, KF = HDC / M::KC, DT = HDC / 32, PF = 16 / M::PR;
+    // Stages, each an array of its own so that the compiler can tell which load
+    // a fragment read waits for: Q tile, dout tile, then lse2 and delta of the rows.
+    constexpr int GO = BQ * T::RB, LO = 2 * GO, DO = LO + 256, SZ = DO + 256;
+    __shared__ __align__(512) unsigned char st0[SZ], st1[SZ];
     __shared__ int flag;
-    __shared__ __align__(16) float l0s[64], d0s[64], l1s[64], d1s[64];  // lse2, delta of the tile's rows
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
-    const int64_t lb = xcd_block_id(blockIdx.x, (int64_t)gridDim.x);
-    const int kvh = (int)(lb / p.ntiles);
-    const int64_t n0b = (lb % p.ntiles) * BK, w0 = n0b + 32 * wave, key = w0 + (lane & 31);
+    const typename T::Lane lofs(lane);
+    const int kvh = (int)(blockIdx.x % p.Hkv);
+    const int64_t tile = heavy_tile<true>(p.seq, p.N, p.ntiles, blockIdx.x / p.Hkv, p.order, reinterpret_cast<int *>(st0), tid);
+    const int64_t n0b = tile * BK, w0 = n0b + 32 * wave, key = w0 + (lane & 31);
 
     int64_t start, end, blk_end;
     const int64_t blk_last = min(n0b + BK, p.N) - 1;
@@ -178,12 +199,17 @@ __global__ __launch_bounds__(256, sizeof(typename E::store_t) == 2 ? 2 : 1) void
     p.seq.find(key < p.N ? key : p.N - 1, start, end);
     const int q_end = (int)blk_end, q0 = (int)n0b;
     const int wfirst_end = __builtin_amdgcn_readlane((int)end, 0);   // rows below it see the wave's first key
-    const int wlast_end = __builtin_amdgcn_readlane((int)end, 31);   // rows at or past it see no key of the wave
+    const int wlast_end = __builtin_amdgcn_readlane((int)end, 31);  // rows at or past it see no key of the wave
     const int ki = (int)key, hi = (int)end;
 
-    frag kf[KF], vf[KF];
+    auto phase = [&]() __attribute__((always_inline)) {
+        if (VL) __builtin_amdgcn_sched_barrier(0);
+    };
+    __shared__ __align__(512) unsigned char vsh[VL ? BK * T::RB : 16];
+    if constexpr (VL) T::template load<BK, NW>(vsh, static_cast<const S *>(p.v) + (int64_t)kvh * p.hd, p.vs, n0b, p.N, p.hd, wave, lane);
+    frag kf[KF], vf[VL ? 1 : KF];
     T::load_row(kf, static_cast<const S *>(p.k) + (int64_t)kvh * p.hd, p.ks, key, p.N, p.hd, lane);
-    T::load_row(vf, static_cast<const S *>(p.v) + (int64_t)kvh * p.hd, p.vs, key, p.N, p.hd, lane);
+    if constexpr (!VL) T::load_row(vf, static_cast<const S *>(p.v) + (int64_t)kvh * p.hd, p.vs, key, p.N, p.hd, lane);
 
     floatx16 dk[DT], dv[DT];
 #pragma unroll
@@ -191,27 +217,34 @@ __global__ __launch_bounds__(256, sizeof(typename E::store_t) == 2 ? 2 : 1) void
 
     const int nt = (q_end - q0 + BQ - 1) / BQ, total = nt * p.G;
     const int64_t os = (int64_t)p.Hq * p.hd;
-    auto issue = [&](int it, unsigned char *qt, unsigned char *gt, float *lt, float *dt) __attribute__((always_inline)) {
-        if (it >= total) return;
-        const int gi = it / nt, m0 = q0 + (it - gi * nt) * BQ;
-        const int64_t qh = (int64_t)kvh * p.G + gi;
-        T::template load<BQ, 4>(qt, static_cast<const S *>(p.q) + qh * p.hd, p.qs, m0, q_end, p.hd, wave, lane);
-        T::template load<BQ, 4>(gt, static_cast<const S *>(p.dout) + qh * p.hd, os, m0, q_end, p.hd, wave, lane);
+    int im0 = q0, ig = 0;  // next tile to load: its first row and head of the group
+    auto issue = [&](unsigned char *st) __attribute__((always_inline)) {
+        if (ig == p.G) return;
+        const int m0 = im0;
+        const int64_t qh = (int64_t)kvh * p.G + ig;
+        im0 += BQ;
+        if (im0 >= q_end) im0 = q0, ++ig;
+        T::template load<BQ, NW>(st, static_cast<const S *>(p.q) + qh * p.hd, p.qs, m0, q_end, p.hd, wave, lane);
+        T::template load<BQ, NW>(st + GO, static_cast<const S *>(p.dout) + qh * p.hd, os, m0, q_end, p.hd, wave, lane);
         if (wave < 2) {
             const float *src = (wave == 0 ? p.lse2 : p.delta) + qh * p.N + m0;
             const __amdgpu_buffer_rsrc_t rs = make_stream(src, 4 * (int64_t)min(BQ, q_end - m0));
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (attn_lds_void *)(wave == 0 ? lt : dt), 4, 4u * lane, 0, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (attn_lds_void *)(st + (wave == 0 ? LO : DO)), 4, 4u * lane, 0, 0, 0);
         }
     };
-    auto compute = [&](int it, const unsigned char *qt, const unsigned char *gt, const float *lt, const float *dt) __attribute__((always_inline)) {
-        const int m0 = q0 + (it % nt) * BQ;
-        if (m0 + BQ <= (int)w0 || m0 >= wlast_end) return;
-        const bool masked = m0 < (int)w0 + 31 || m0 + BQ > wfirst_end;
+    auto compute = [&](bool masked, int m0, const unsigned char *qt) __attribute__((always_inline)) {
+        const unsigned char *gt = qt + GO;
+        const float *lt = reinterpret_cast<const float *>(qt + LO), *dt = reinterpret_cast<const float *>(qt + DO);
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
+            const typename T::Lane ln = lofs.fresh();
             floatx16 s = zero16(), dp = zero16();
 #pragma unroll
-            for (int kc = 0; kc < KF; ++kc) s = M::mul(T::read_row(qt, 32 * j, kc, lane), kf[kc], s);
+            for (int kc = 0; kc < KF; ++kc) {
+                s = M::mul(T::read_row(qt, 32 * j, kc, ln), kf[kc], s);
+            }
+            frag pf[PF];
+            phase();
 #pragma unroll
             for (int i = 0; i < 16; i += 4) {
                 const float4 l = *reinterpret_cast<const float4 *>(lt + 32 * j + res_row(i, h));
@@ -220,24 +253,28 @@ __global__ __launch_bounds__(256, sizeof(typename E::store_t) == 2 ? 2 : 1) void
                 s[i + 2] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i + 2], p.c2, -l.z));
                 s[i + 3] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i + 3], p.c2, -l.w));
             }
-            uint32_t open = 0xffffu;  // rows of this lane's elements that see its key
             if (masked) {
-                open = 0;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const int qr = m0 + 32 * j + res_row(i, h);
-                    if (qr >= ki && qr < hi) open |= 1u << i;
-                    else s[i] = 0.f;
+                    if (qr < ki || qr >= hi) s[i] = 0.f;
                 }
             }
 #pragma unroll
-            for (int f = 0; f < PF; ++f) {
-                const frag pf = M::pack(s, f);
+            for (int f = 0; f < PF; ++f) pf[f] = M::pack(s, f);
+            phase();
 #pragma unroll
-                for (int d = 0; d < DT; ++d) dv[d] = M::mul(T::read_tr(gt, 32 * j, f, d, lane), pf, dv[d]);
+            for (int f = 0; f < PF; ++f)
+#pragma unroll
+                for (int d = 0; d < DT; ++d) dv[d] = M::mul(T::read_tr(gt, 32 * j, f, d, ln), pf[f], dv[d]);
+            phase();
+#pragma unroll
+            for (int kc = 0; kc < KF; ++kc) {
+                const frag x = T::read_row(gt, 32 * j, kc, ln);
+                if constexpr (VL) dp = M::mul(x, T::read_row(vsh, 32 * wave, kc, ln), dp);
+                else dp = M::mul(x, vf[kc], dp);
             }
-#pragma unroll
-            for (int kc = 0; kc < KF; ++kc) dp = M::mul(T::read_row(gt, 32 * j, kc, lane), vf[kc], dp);
+            phase();
 #pragma unroll
             for (int i = 0; i < 16; i += 4) {
                 const float4 dl = *reinterpret_cast<const float4 *>(dt + 32 * j + res_row(i, h));
@@ -246,17 +283,20 @@ __global__ __launch_bounds__(256, sizeof(typename E::store_t) == 2 ? 2 : 1) void
                 s[i + 2] *= dp[i + 2] - dl.z;
                 s[i + 3] *= dp[i + 3] - dl.w;
             }
-            if (masked) {
+            if (masked) {  // zero times a non-finite difference is not zero
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (!((open >> i) & 1)) s[i] = 0.f;
+                for (int i = 0; i < 16; ++i) {
+                    const int qr = m0 + 32 * j + res_row(i, h);
+                    if (qr < ki || qr >= hi) s[i] = 0.f;
+                }
             }
 #pragma unroll
-            for (int f = 0; f < PF; ++f) {
-                const frag df = M::pack(s, f);
+            for (int f = 0; f < PF; ++f) pf[f] = M::pack(s, f);
+            phase();
 #pragma unroll
-                for (int d = 0; d < DT; ++d) dk[d] = M::mul(T::read_tr(qt, 32 * j, f, d, lane), df, dk[d]);
-            }
+            for (int f = 0; f < PF; ++f)
+#pragma unroll
+                for (int d = 0; d < DT; ++d) dk[d] = M::mul(T::read_tr(qt, 32 * j, f, d, ln), pf[f], dk[d]);
         }
     };
     // Rows of a tile with masked pairs that are not finite are left out of its
@@ -264,35 +304,42 @@ __global__ __launch_bounds__(256, sizeof(typename E::store_t) == 2 ? 2 : 1) void
     // row's lse (q) or delta (dout); dv gets the row's values after the walk.
     bool spoilt = false;
     auto tile_masked = [&](int m0) { return m0 < (int)n0b + BK - 1 || m0 + BQ > blk_first_end; };
-    auto step = [&](int it, unsigned char *qt, unsigned char *gt, float *lt, float *dt, unsigned char *qn,
-                    unsigned char *gn, float *ln, float *dn) __attribute__((always_inline)) {
+    // A tile's loads are waited for, then a barrier shows them to every wave
+    // and ends every wave's reads of the other stage, which is refilled.
+    int cm0 = q0;  // first row of the tile worked on
+    auto step = [&](int it, unsigned char *cur, unsigned char *refill) __attribute__((always_inline)) {
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        issue(it + 1, qn, gn, ln, dn);
-        const int m0 = q0 + (it % nt) * BQ;
-        if (tile_masked(m0) && tile_dirty<T, BQ, 4, true>(qt, gt, &flag, it, wave, lane)) spoilt = true;
-        compute(it, qt, gt, lt, dt);
+        issue(refill);
+        const int m0 = cm0;
+        cm0 = cm0 + BQ >= q_end ? q0 : cm0 + BQ;
+        if (tile_masked(m0) && tile_dirty<T, BQ, NW, true>(cur, cur + GO, &flag, it, wave, lane)) spoilt = true;
+        if (m0 + BQ <= (int)w0 || m0 >= wlast_end) return;  // no row of the tile sees a key of the wave
+        compute(m0 < (int)w0 + 31 || m0 + BQ > wfirst_end, m0, cur);
     };
-    issue(0, q0s, g0s, l0s, d0s);
+    issue(st0);
     for (int it = 0; it < total; it += 2) {
-        step(it, q0s, g0s, l0s, d0s, q1s, g1s, l1s, d1s);
-        if (it + 1 < total) step(it + 1, q1s, g1s, l1s, d1s, q0s, g0s, l0s, d0s);
+        step(it, st0, st1);
+        if (it + 1 < total) step(it + 1, st1, st0);
     }
-    T::store_row(dk, p.scale, static_cast<S *>(p.dk) + (int64_t)kvh * p.hd, p.dks, key, p.N, p.hd, lane);
     S *dvb = static_cast<S *>(p.dv) + (int64_t)kvh * p.hd;
+    T::store_row(dk, p.scale, static_cast<S *>(p.dk) + (int64_t)kvh * p.hd, p.dks, key, p.N, p.hd, lane);
     T::store_row(dv, 1.f, dvb, p.dvs, key, p.N, p.hd, lane);
     if (__builtin_expect(spoilt, 0))
         for (int gi = 0; gi < p.G; ++gi)
-            T::add_nonfinite(dvb, p.dvs, key, p.N, p.hd,
-                             static_cast<const S *>(p.dout) + ((int64_t)kvh * p.G + gi) * p.hd, os, q0, q_end, lane,
-                             [&](int r) { return r >= ki && r < hi && tile_masked(r - (r - q0) % BQ); });
+            T::add_nonfinite(
+                dvb, p.dvs, key, p.N, p.hd, static_cast<const S *>(p.dout) + ((int64_t)kvh * p.G + gi) * p.hd, os, q0,
+                q_end, lane,
+                [&](int r) { return r >= ki && r < hi && tile_masked(r - (r - q0) % BQ); });
 }
 
 template <class E, int HDC>
 void launch(const BwdParams &p, hipStream_t s) {
     hipLaunchKernelGGL((attn_dq_kernel<E, HDC>), dim3((unsigned)(p.ntiles * p.Hq)), dim3(256), 0, s, p);
-    hipLaunchKernelGGL((attn_dkv_kernel<E, HDC>), dim3((unsigned)(p.ntiles * p.Hkv)), dim3(256), 0, s, p);
+    using C = DkvCfg<E, HDC>;
+    static_assert(32 * C::NW == 128, "tiles of 128 keys");
+    hipLaunchKernelGGL((attn_dkv_kernel<E, HDC>), dim3((unsigned)(p.ntiles * p.Hkv)), dim3(64 * C::NW), 0, s, p);
 }
 
 template <class E>
@@ -310,7 +357,8 @@ hipError_t attn_bwd(const AttnProblem &a, hipStream_t s) {
     float *delta = static_cast<float *>(a.ws);
     BwdParams p{a.q, a.k, a.v, a.o, a.dout, a.lse, a.dq, a.dk, a.dv, delta, delta + a.N * a.Hq,
                 SeqMap{a.cu, a.n_seqs, a.T}, a.N, a.qs, a.ks, a.vs, a.dqs, a.dks, a.dvs, a.Hq, a.Hkv,
-                a.Hq / a.Hkv, a.hd, a.scale, a.scale * kLog2e, (a.N + 127) / 128};
+                a.Hq / a.Hkv, a.hd, a.scale, a.scale * kLog2e, (a.N + 127) / 128, false};
+    p.order = p.ntiles * p.Hkv > device_cus();  // with a block or less per CU all start at once
     if (a.dtype == Dtype::BF16) dispatch<BF16>(p, s);
     else dispatch<F32>(p, s);
     return hipGetLastError();

@@ -118,32 +118,49 @@ struct Tile {
         }
     }
 
-    // Fragment kc of row r0 + lane%32: channels KC*kc ...
-    __device__ __forceinline__ static frag read_row(const unsigned char *lds, int r0, int kc, int lane) {
-        const int r = r0 + (lane & 31);
-        return *reinterpret_cast<const frag *>(lds + r * RB + 16 * ((2 * kc + (lane >> 5)) ^ swz(r)));
+    // Byte offsets from which a lane's fragment addresses follow by an
+    // exclusive or and an addition of constants (a tile's base is a multiple of
+    // RB, its chunk places lie below).  fresh() hides their values: hoisted out
+    // of the tile loop, the addresses would take some 30 registers.
+    struct Lane {
+        uint32_t row, tr;
+        __device__ __forceinline__ explicit Lane(int lane) {
+            const int r = lane & 31, h = lane >> 5;
+            row = r * RB + 16 * (h ^ swz(r));
+            if constexpr (sizeof(S) == 2) {
+                // a 16-lane group reads a 4 x 16 block, lane i its 8-byte piece i, and gets column i
+                const int i = lane & 15, q = 4 * h + (i >> 2), c = ((lane >> 3) & 2) + ((i >> 1) & 1);
+                tr = q * RB + 16 * (c ^ swz(q)) + 8 * (i & 1);
+            } else {
+                tr = 4 * h * RB + 16 * ((r >> 2) ^ (4 * h)) + 4 * (r & 3);
+            }
+        }
+        __device__ __forceinline__ Lane fresh() const {
+            Lane l = *this;
+            asm volatile("" : "+v"(l.row), "+v"(l.tr));
+            return l;
+        }
+    };
+
+    // Fragment kc of row r0 + lane%32 (r0 a multiple of 32): channels KC*kc ...
+    __device__ __forceinline__ static frag read_row(const unsigned char *lds, int r0, int kc, const Lane &l) {
+        return *reinterpret_cast<const frag *>(lds + r0 * RB + (l.row ^ (32u * kc)));
     }
 
     // Fragment of the transposed tile: channel 32*dt + lane%32, the rows of
-    // result fragment f counted from r0 (a multiple of 16).
-    __device__ __forceinline__ static frag read_tr(const unsigned char *lds, int r0, int f, int dt, int lane) {
+    // result fragment f counted from r0 (a multiple of 32).
+    __device__ __forceinline__ static frag read_tr(const unsigned char *lds, int r0, int f, int dt, const Lane &l) {
         if constexpr (sizeof(S) == 2) {
-            // a 16-lane group reads a 4 x 16 block, lane i its 8-byte piece i, and gets column i
-            const int i = lane & 15, r = r0 + 16 * f + 4 * (lane >> 5) + (i >> 2);
-            const int c = 4 * dt + ((lane >> 3) & 2) + ((i >> 1) & 1);
-            const unsigned char *p0 = lds + r * RB + 16 * (c ^ swz(r)) + 8 * (i & 1);
-            const unsigned char *p1 = lds + (r + 8) * RB + 16 * (c ^ swz(r + 8)) + 8 * (i & 1);
-            const shortx4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((attn_lds_s4 *)p0);
-            const shortx4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((attn_lds_s4 *)p1);
+            constexpr uint32_t X8 = RS == 64 ? 32 : 128;  // swz(r + 8) ^ swz(r), in bytes
+            const unsigned char *p = lds + (r0 + 16 * f) * RB;
+            const shortx4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((attn_lds_s4 *)(p + (l.tr ^ (64u * dt))));
+            const shortx4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((attn_lds_s4 *)(p + 8 * RB + (l.tr ^ (64u * dt) ^ X8)));
             return __builtin_bit_cast(frag, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
         } else {
-            const int d = 32 * dt + (lane & 31);
             frag v;
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const int r = r0 + 8 * f + 4 * (lane >> 5) + s;
-                v[s] = *reinterpret_cast<const float *>(lds + r * RB + 16 * ((d >> 2) ^ swz(r)) + 4 * (d & 3));
-            }
+            for (int s = 0; s < 4; ++s)
+                v[s] = *reinterpret_cast<const float *>(lds + (r0 + 8 * f + s) * RB + 128 * dt + (l.tr ^ (16u * s)));
             return v;
         }
     }
@@ -291,6 +308,82 @@ __device__ __forceinline__ bool tile_dirty(unsigned char *a, unsigned char *b, i
         lds_barrier();
     }
     return dirty;
+}
+
+// Tile of 128 token rows that a block takes as number `rank` of its head.
+// Tiles differ in work (the rows before them in their sequence, or after them
+// with KEYS), and blocks start in grid order, so the heaviest tiles go first
+// and the light ones fill the gaps at the end: at 2 to 8 rounds of blocks the
+// order of the tokens left 13 to 33% of the CUs idle.  Rows of whole tiles
+// have a closed form.  Otherwise every block counts the tiles' weights in LDS
+// and picks the rank-th by weight, then by index (lds: kRankInts ints; at most
+// kRankTiles tiles, more keep the reverse order).  Every block of a head gets
+// a tile of its own, whatever the weights.  Ends with a barrier.
+constexpr int kRankTiles = 1024, kRankInts = 256 + 4 + 16;
+template <bool KEYS>
+__device__ __forceinline__ int heavy_tile(const SeqMap &seq, int64_t N, int64_t ntiles, int64_t rank, bool order, int *lds,
+                                          int tid) {
+    if (!order) return (int)(KEYS ? rank : ntiles - 1 - rank);
+    if (seq.cu == nullptr && seq.T % 128 == 0) {
+        const int64_t per = seq.T / 128, rows = N / seq.T, at = rank / rows;
+        return (int)((rank % rows) * per + (KEYS ? at : per - 1 - at));
+    }
+    if (ntiles > kRankTiles) return (int)(KEYS ? rank : ntiles - 1 - rank);
+    const int lane = tid & 63, wave = tid >> 6;
+    lds[tid] = 0;
+    __syncthreads();
+    int w[kRankTiles / 256];
+#pragma unroll
+    for (int c = 0; c < kRankTiles / 256; ++c) {
+        const int t = 256 * c + tid;
+        w[c] = -1;
+        if (t < ntiles) {
+            int64_t a, b;
+            const int64_t m0 = 128 * (int64_t)t, last = min(m0 + 128, N) - 1;
+            seq.find(KEYS ? last : m0, a, b);
+            w[c] = (int)min((int64_t)255, (KEYS ? b - m0 : last - a) / 128);
+            atomicAdd(&lds[w[c]], 1);
+        }
+    }
+    __syncthreads();
+    if (wave == 0) {  // lane l: the four weights 255 - 4l .. 252 - 4l
+        int n = 0, before;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) n += lds[255 - 4 * lane - i];
+        int upto = n;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int v = __shfl_up(upto, d);
+            if (lane >= d) upto += v;
+        }
+        before = upto - n;
+        if (before <= rank && rank < upto) {
+            int left = (int)rank - before, b = 255 - 4 * lane;
+            while (left >= lds[b]) left -= lds[b--];
+            lds[256] = b;
+            lds[257] = left;
+        }
+    }
+    __syncthreads();
+    const int b = lds[256], k = lds[257];
+    uint64_t m[kRankTiles / 256];
+#pragma unroll
+    for (int c = 0; c < kRankTiles / 256; ++c) {
+        m[c] = __ballot(w[c] == b);
+        if (lane == 0) lds[260 + 4 * c + wave] = __popcll(m[c]);
+    }
+    __syncthreads();
+    int base = 0;
+#pragma unroll
+    for (int i = 0; i < kRankTiles / 64; ++i) {
+        const int c = i / 4;
+        if (i % 4 == wave && w[c] == b && base + __popcll(m[c] & ((1ull << lane) - 1)) == k) lds[258] = 256 * c + tid;
+        base += lds[260 + i];
+    }
+    __syncthreads();
+    const int t = __builtin_amdgcn_readfirstlane(lds[258]);
+    __syncthreads();  // the ints may be overwritten from here
+    return t;
 }
 
 constexpr float kLog2e = 1.44269504088896340736f;

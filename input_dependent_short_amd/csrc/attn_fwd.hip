@@ -26,6 +26,7 @@ struct FwdParams {
     int32_t Hq, Hkv, G, hd;
     float c2;  // scale * log2(e)
     int64_t ntiles;
+    bool order;  // heaviest tiles first
 };
 
 template <class E>
@@ -38,16 +39,15 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdParams p) {
     using S = typename E::store_t;
     using frag = typename M::frag;
     constexpr int BN = kBN<E>, BM = 128, NS = BN / 32, KF = HDC / M::KC, DT = HDC / 32, PF = 16 / M::PR;
-    __shared__ __align__(16) unsigned char k0s[BN * T::RB], v0s[BN * T::RB], k1s[BN * T::RB], v1s[BN * T::RB];
+    __shared__ __align__(512) unsigned char k0s[BN * T::RB], v0s[BN * T::RB], k1s[BN * T::RB], v1s[BN * T::RB];
     __shared__ int flag;
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
-    const int64_t lb = xcd_block_id(blockIdx.x, (int64_t)gridDim.x);
-    const int g = (int)(lb % p.G);
-    const int64_t rest = lb / p.G;
-    const int kvh = (int)(rest / p.ntiles);
-    const int64_t tile = p.ntiles - 1 - rest % p.ntiles;
-    const int qh = kvh * p.G + g;
+    const typename T::Lane lofs(lane);
+    // Key head fastest: blocks b, b + 8, ... share an XCD, so with a multiple
+    // of eight key heads each one's keys and values stay in one XCD's L2.
+    const int head = (int)(blockIdx.x % p.Hq), kvh = head % p.Hkv, qh = kvh * p.G + head / p.Hkv;
+    const int64_t tile = heavy_tile<false>(p.seq, p.N, p.ntiles, blockIdx.x / p.Hq, p.order, reinterpret_cast<int *>(k0s), tid);
     const int64_t m0 = tile * BM, w0 = m0 + 32 * wave, row = w0 + (lane & 31);
 
     // sequence starts: the block's first row, this lane's row, the wave's last row
@@ -79,16 +79,16 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdParams p) {
         T::template load<BN, 4>(ks, kb, p.ks, n0, kv_end, p.hd, wave, lane);
         T::template load<BN, 4>(vs, vb, p.vs, n0, kv_end, p.hd, wave, lane);
     };
-    auto compute = [&](int n0, const unsigned char *ks, const unsigned char *vs) __attribute__((always_inline)) {
-        if (n0 > wlast || n0 + BN <= wfirst_key) return;
+    auto compute = [&](bool masked, int n0, const unsigned char *ks, const unsigned char *vs) __attribute__((always_inline)) {
+        const typename T::Lane ln = lofs.fresh();
         floatx16 s[NS];
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
             s[j] = zero16();
 #pragma unroll
-            for (int kc = 0; kc < KF; ++kc) s[j] = M::mul(T::read_row(ks, 32 * j, kc, lane), qf[kc], s[j]);
+            for (int kc = 0; kc < KF; ++kc) s[j] = M::mul(T::read_row(ks, 32 * j, kc, ln), qf[kc], s[j]);
         }
-        if (n0 + BN - 1 > (int)w0 || n0 < wlast_start) {  // some pair of the tile is masked
+        if (masked) {
 #pragma unroll
             for (int j = 0; j < NS; ++j)
 #pragma unroll
@@ -128,11 +128,11 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdParams p) {
             for (int f = 0; f < PF; ++f) {
                 const frag pf = M::pack(s[j], f);
 #pragma unroll
-                for (int d = 0; d < DT; ++d) acc[d] = M::mul(T::read_tr(vs, 32 * j, f, d, lane), pf, acc[d]);
+                for (int d = 0; d < DT; ++d) acc[d] = M::mul(T::read_tr(vs, 32 * j, f, d, ln), pf, acc[d]);
             }
     };
     bool spoilt = false;  // V rows of a tile with masked pairs held non-finite values, left out of the product
-    auto masked = [&](int n0) { return n0 + BN - 1 > (int)m0 || n0 < blk_last_start; };
+    auto tile_masked = [&](int n0) { return n0 + BN - 1 > (int)m0 || n0 < blk_last_start; };
     // A tile's loads are waited for, then a barrier shows them to every wave
     // and ends every wave's reads of the other stage, which is refilled.
     auto step = [&](int n0, unsigned char *ks, unsigned char *vs, unsigned char *kn,
@@ -141,8 +141,9 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdParams p) {
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         issue(n0 + BN, kn, vn);
-        if (masked(n0) && tile_dirty<T, BN, 4, true>(vs, nullptr, &flag, n0, wave, lane)) spoilt = true;
-        compute(n0, ks, vs);
+        if (tile_masked(n0) && tile_dirty<T, BN, 4, true>(vs, nullptr, &flag, n0, wave, lane)) spoilt = true;
+        if (n0 > wlast || n0 + BN <= wfirst_key) return;  // no key of the tile is seen by the wave
+        compute(n0 + BN - 1 > (int)w0 || n0 < wlast_start, n0, ks, vs);
     };
     issue(kv0, k0s, v0s);
     for (int n0 = kv0; n0 < kv_end; n0 += 2 * BN) {
@@ -156,7 +157,7 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdParams p) {
     T::store_row(acc, inv, ob, (int64_t)p.Hq * p.hd, row, p.N, p.hd, lane);
     if (__builtin_expect(spoilt, 0))
         T::add_nonfinite(ob, (int64_t)p.Hq * p.hd, row, p.N, p.hd, vb, p.vs, kv0, kv_end, lane, [&](int r) {
-            return r <= qi && r >= lo && masked(r - (r - kv0) % BN);
+            return r <= qi && r >= lo && tile_masked(r - (r - kv0) % BN);
         });
     if (p.lse && h == 0 && row < p.N) p.lse[(int64_t)qh * p.N + row] = mx * p.c2 * kLn2 + __logf(sum);
 }
@@ -178,7 +179,8 @@ void dispatch(const FwdParams &p, hipStream_t s) {
 
 hipError_t attn_fwd(const AttnProblem &a, hipStream_t s) {
     FwdParams p{a.q, a.k, a.v, a.o, a.lse, SeqMap{a.cu, a.n_seqs, a.T}, a.N, a.qs, a.ks, a.vs, a.Hq, a.Hkv,
-                a.Hq / a.Hkv, a.hd, a.scale * kLog2e, (a.N + 127) / 128};
+                a.Hq / a.Hkv, a.hd, a.scale * kLog2e, (a.N + 127) / 128, false};
+    p.order = p.ntiles * p.Hq > device_cus();  // with a block or less per CU all start at once
     if (a.dtype == Dtype::BF16) dispatch<BF16>(p, s);
     else dispatch<F32>(p, s);
     return hipGetLastError();
