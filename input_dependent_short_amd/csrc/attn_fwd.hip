@@ -32,6 +32,13 @@ struct FwdParams {
 template <class E>
 constexpr int kBN = sizeof(typename E::store_t) == 2 ? 64 : 32;  // keys per tile
 
+// Heads of up to 64 channels fit four blocks per CU with two K stages.  Wider
+// ones keep a single K stage, refilled after a second barrier once the scores
+// are formed: 48 instead of 64 KB of LDS, three blocks per CU (packed ~2B
+// shape: 400 against 418 us; ~150M shape: 80 against 78 us).
+template <int HDC>
+constexpr bool kTwoK = HDC <= 64;
+
 template <class E, int HDC>
 __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdParams p) {
     using T = Tile<E, HDC>;
@@ -39,7 +46,8 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdParams p) {
     using S = typename E::store_t;
     using frag = typename M::frag;
     constexpr int BN = kBN<E>, BM = 128, NS = BN / 32, KF = HDC / M::KC, DT = HDC / 32, PF = 16 / M::PR;
-    __shared__ __align__(512) unsigned char k0s[BN * T::RB], v0s[BN * T::RB], k1s[BN * T::RB], v1s[BN * T::RB];
+    __shared__ __align__(512) unsigned char k0s[BN * T::RB], k1s[kTwoK<HDC> ? BN * T::RB : 16], v0s[BN * T::RB],
+        v1s[BN * T::RB];
     __shared__ int flag;
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
@@ -72,12 +80,23 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdParams p) {
     floatx16 acc[DT];
 #pragma unroll
     for (int d = 0; d < DT; ++d) acc[d] = zero16();
-    float mx = -INFINITY, sum = 0.f;  // running maximum (both halves) of the raw scores, this half's sum
+    float mx = -INFINITY, sum = 0.f;  // reference maximum (both halves) of the raw scores, this half's sum
+    // A row's reference is raised, and its sums rescaled, only when the maximum
+    // passes it by more than 8 / c2: the probabilities are then at most 2^8,
+    // far inside fp32 and bf16, and most tiles skip the rescaling.
+    const float slack = 8.f / p.c2;
 
-    auto issue = [&](int n0, unsigned char *ks, unsigned char *vs) __attribute__((always_inline)) {
-        if (n0 >= kv_end) return;
-        T::template load<BN, 4>(ks, kb, p.ks, n0, kv_end, p.hd, wave, lane);
-        T::template load<BN, 4>(vs, vb, p.vs, n0, kv_end, p.hd, wave, lane);
+    auto load_k = [&](int n0, unsigned char *ks) __attribute__((always_inline)) {
+        if (n0 < kv_end) T::template load<BN, 4>(ks, kb, p.ks, n0, kv_end, p.hd, wave, lane);
+    };
+    auto load_v = [&](int n0, unsigned char *vs) __attribute__((always_inline)) {
+        if (n0 < kv_end) T::template load<BN, 4>(vs, vb, p.vs, n0, kv_end, p.hd, wave, lane);
+    };
+    // Every wave is done with what it read from LDS, and sees what the others wrote.
+    auto barrier = [&]() __attribute__((always_inline)) {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
     };
     auto compute = [&](bool masked, int n0, const unsigned char *ks, const unsigned char *vs) __attribute__((always_inline)) {
         const typename T::Lane ln = lofs.fresh();
@@ -87,6 +106,10 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdParams p) {
             s[j] = zero16();
 #pragma unroll
             for (int kc = 0; kc < KF; ++kc) s[j] = M::mul(T::read_row(ks, 32 * j, kc, ln), qf[kc], s[j]);
+        }
+        if constexpr (!kTwoK<HDC>) {
+            barrier();
+            load_k(n0 + BN, k0s);
         }
         if (masked) {
 #pragma unroll
@@ -103,8 +126,9 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdParams p) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) top = fmaxf(top, s[j][i]);
         top = fmaxf(top, other_half(top));
-        if (__any(top > mx)) {
-            const float nm = fmaxf(mx, top);
+        const bool raise = top > mx + slack;
+        if (__any(raise)) {  // the other rows are multiplied by one: a row's bits do not depend on its neighbours
+            const float nm = raise ? top : mx;
             const float safe = nm == -INFINITY ? 0.f : nm;
             const float al = __builtin_amdgcn_exp2f((mx - safe) * p.c2);
             mx = nm;
@@ -134,21 +158,29 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdParams p) {
     bool spoilt = false;  // V rows of a tile with masked pairs held non-finite values, left out of the product
     auto tile_masked = [&](int n0) { return n0 + BN - 1 > (int)m0 || n0 < blk_last_start; };
     // A tile's loads are waited for, then a barrier shows them to every wave
-    // and ends every wave's reads of the other stage, which is refilled.
+    // and ends every wave's reads of the stages that are refilled.
     auto step = [&](int n0, unsigned char *ks, unsigned char *vs, unsigned char *kn,
                     unsigned char *vn) __attribute__((always_inline)) {
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-        issue(n0 + BN, kn, vn);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        barrier();
+        if constexpr (kTwoK<HDC>) load_k(n0 + BN, kn);
+        load_v(n0 + BN, vn);
         if (tile_masked(n0) && tile_dirty<T, BN, 4, true>(vs, nullptr, &flag, n0, wave, lane)) spoilt = true;
-        if (n0 > wlast || n0 + BN <= wfirst_key) return;  // no key of the tile is seen by the wave
+        if (n0 > wlast || n0 + BN <= wfirst_key) {  // no key of the tile is seen by the wave
+            if constexpr (!kTwoK<HDC>) {
+                barrier();
+                load_k(n0 + BN, k0s);
+            }
+            return;
+        }
         compute(n0 + BN - 1 > (int)w0 || n0 < wlast_start, n0, ks, vs);
     };
-    issue(kv0, k0s, v0s);
+    unsigned char *const kb1 = kTwoK<HDC> ? k1s : k0s;
+    load_k(kv0, k0s);
+    load_v(kv0, v0s);
     for (int n0 = kv0; n0 < kv_end; n0 += 2 * BN) {
-        step(n0, k0s, v0s, k1s, v1s);
-        if (n0 + BN < kv_end) step(n0 + BN, k1s, v1s, k0s, v0s);
+        step(n0, k0s, v0s, kb1, v1s);
+        if (n0 + BN < kv_end) step(n0 + BN, kb1, v1s, k0s, v0s);
     }
 
     sum += other_half(sum);
