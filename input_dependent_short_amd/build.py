@@ -31,6 +31,7 @@ FLAGS = [
 FILE_FLAGS = {
     "lowrank_fwd.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "attn_bwd.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+    "attn_short.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
 }
 
 

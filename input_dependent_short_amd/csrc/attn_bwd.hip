@@ -18,19 +18,6 @@
 namespace dsc {
 namespace {
 
-struct BwdParams {
-    const void *q, *k, *v, *o, *dout;
-    const float *lse;
-    void *dq, *dk, *dv;
-    float *delta, *lse2;  // workspace (Hq, N) each
-    SeqMap seq;
-    int64_t N, qs, ks, vs, dqs, dks, dvs;
-    int32_t Hq, Hkv, G, hd;
-    float scale, c2;
-    int64_t ntiles;
-    bool order;  // heaviest tiles first
-};
-
 template <class E>
 constexpr int kBT = sizeof(typename E::store_t) == 2 ? 64 : 32;  // rows per walked tile
 
@@ -75,16 +62,7 @@ __global__ __launch_bounds__(256, sizeof(typename E::store_t) == 2 ? 2 : 1) void
     const int64_t os = (int64_t)p.Hq * p.hd;
     T::load_row(qf, static_cast<const S *>(p.q) + (int64_t)qh * p.hd, p.qs, row, p.N, p.hd, lane);
     T::load_row(gf, static_cast<const S *>(p.dout) + (int64_t)qh * p.hd, os, row, p.N, p.hd, lane);
-    float delta = 0.f;
-    {
-        frag of[KF];
-        T::load_row(of, static_cast<const S *>(p.o) + (int64_t)qh * p.hd, os, row, p.N, p.hd, lane);
-#pragma unroll
-        for (int kc = 0; kc < KF; ++kc)
-#pragma unroll
-            for (int j = 0; j < T::VEC; ++j) delta = __builtin_fmaf((float)gf[kc][j], (float)of[kc][j], delta);
-    }
-    delta += other_half(delta);
+    const float delta = row_delta<T>(gf, static_cast<const S *>(p.o) + (int64_t)qh * p.hd, os, row, p.N, p.hd, lane);
     const float lse2 = row < p.N ? p.lse[(int64_t)qh * p.N + row] * kLog2e : 0.f;
     if (h == 0 && row < p.N) {
         p.delta[(int64_t)qh * p.N + row] = delta;
@@ -335,18 +313,17 @@ __global__ __launch_bounds__((64 * DkvCfg<E, HDC>::NW), (DkvCfg<E, HDC>::kOcc)) 
 }
 
 template <class E, int HDC>
-void launch(const BwdParams &p, hipStream_t s) {
-    hipLaunchKernelGGL((attn_dq_kernel<E, HDC>), dim3((unsigned)(p.ntiles * p.Hq)), dim3(256), 0, s, p);
-    using C = DkvCfg<E, HDC>;
-    static_assert(32 * C::NW == 128, "tiles of 128 keys");
-    hipLaunchKernelGGL((attn_dkv_kernel<E, HDC>), dim3((unsigned)(p.ntiles * p.Hkv)), dim3(64 * C::NW), 0, s, p);
+void launch(const BwdParams &p, hipStream_t s, bool dq, bool dkv) {
+    static_assert(DkvCfg<E, HDC>::NW == 4, "tiles of 128 keys");
+    if (dq) hipLaunchKernelGGL((attn_dq_kernel<E, HDC>), dim3((unsigned)(p.ntiles * p.Hq)), dim3(256), 0, s, p);
+    if (dkv) hipLaunchKernelGGL((attn_dkv_kernel<E, HDC>), dim3((unsigned)(p.ntiles * p.Hkv)), dim3(256), 0, s, p);
 }
 
 template <class E>
-void dispatch(const BwdParams &p, hipStream_t s) {
-    if (p.hd <= 64) launch<E, 64>(p, s);
-    else if (p.hd <= 96) launch<E, 96>(p, s);
-    else launch<E, 128>(p, s);
+void dispatch(const BwdParams &p, hipStream_t s, bool dq, bool dkv) {
+    if (p.hd <= 64) launch<E, 64>(p, s, dq, dkv);
+    else if (p.hd <= 96) launch<E, 96>(p, s, dq, dkv);
+    else launch<E, 128>(p, s, dq, dkv);
 }
 
 }  // namespace
@@ -359,8 +336,16 @@ hipError_t attn_bwd(const AttnProblem &a, hipStream_t s) {
                 SeqMap{a.cu, a.n_seqs, a.T}, a.N, a.qs, a.ks, a.vs, a.dqs, a.dks, a.dvs, a.Hq, a.Hkv,
                 a.Hq / a.Hkv, a.hd, a.scale, a.scale * kLog2e, (a.N + 127) / 128, false};
     p.order = p.ntiles * p.Hkv > device_cus();  // with a block or less per CU all start at once
-    if (a.dtype == Dtype::BF16) dispatch<BF16>(p, s);
-    else dispatch<F32>(p, s);
+    const bool few_q = attn_few_rows(p.ntiles * p.Hq, p.seq, p.N),
+               few_k = attn_few_rows(p.ntiles * p.Hkv, p.seq, p.N);
+    auto run = [&](bool dq, bool dkv) {
+        if (a.dtype == Dtype::BF16) dispatch<BF16>(p, s, dq, dkv);
+        else dispatch<F32>(p, s, dq, dkv);
+    };
+    if (few_q) attn_dq_short(p, a.dtype, s);  // leaves delta and lse2 for the other
+    else run(true, false);
+    if (few_k) attn_dkv_short(p, a.dtype, s);
+    else run(false, true);
     return hipGetLastError();
 }
 

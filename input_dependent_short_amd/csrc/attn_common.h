@@ -386,6 +386,53 @@ __device__ __forceinline__ int heavy_tile(const SeqMap &seq, int64_t N, int64_t 
     return t;
 }
 
+// <dout, o> of this lane's row (lane%32), in both halves; gf holds dout.
+template <class T, int KF>
+__device__ __forceinline__ float row_delta(const typename T::frag (&gf)[KF], const typename T::S *o, int64_t stride,
+                                           int64_t row, int64_t N, int hd, int lane) {
+    typename T::frag of[KF];
+    T::load_row(of, o, stride, row, N, hd, lane);
+    float d = 0.f;
+#pragma unroll
+    for (int kc = 0; kc < KF; ++kc)
+#pragma unroll
+        for (int j = 0; j < T::VEC; ++j) d = __builtin_fmaf((float)gf[kc][j], (float)of[kc][j], d);
+    return d + other_half(d);
+}
+
+// Kernel arguments of the forward and of the backward.
+struct FwdParams {
+    const void *q, *k, *v;
+    void *o;
+    float *lse;
+    SeqMap seq;
+    int64_t N, qs, ks, vs;
+    int32_t Hq, Hkv, G, hd;
+    float c2;  // scale * log2(e)
+    int64_t ntiles;
+    bool order;  // heaviest tiles first
+};
+
+struct BwdParams {
+    const void *q, *k, *v, *o, *dout;
+    const float *lse;
+    void *dq, *dk, *dv;
+    float *delta, *lse2;  // workspace (Hq, N) each
+    SeqMap seq;
+    int64_t N, qs, ks, vs, dqs, dks, dvs;
+    int32_t Hq, Hkv, G, hd;
+    float scale, c2;
+    int64_t ntiles;
+    bool order;  // heaviest tiles first
+};
+
+// attn_short.hip: the same results for inputs of few rows; blocks counts the
+// blocks of 128 rows that the kernel for long inputs would run.
+bool attn_few_rows(int64_t blocks, const SeqMap &seq, int64_t N);
+void attn_fwd_short(FwdParams p, Dtype dt, hipStream_t s);
+void attn_dq_short(BwdParams p, Dtype dt, hipStream_t s);
+void attn_dkv_short(BwdParams p, Dtype dt, hipStream_t s);
+
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 

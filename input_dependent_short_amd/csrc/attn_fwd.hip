@@ -17,18 +17,6 @@
 namespace dsc {
 namespace {
 
-struct FwdParams {
-    const void *q, *k, *v;
-    void *o;
-    float *lse;
-    SeqMap seq;
-    int64_t N, qs, ks, vs;
-    int32_t Hq, Hkv, G, hd;
-    float c2;  // scale * log2(e)
-    int64_t ntiles;
-    bool order;  // heaviest tiles first
-};
-
 template <class E>
 constexpr int kBN = sizeof(typename E::store_t) == 2 ? 64 : 32;  // keys per tile
 
@@ -213,7 +201,8 @@ hipError_t attn_fwd(const AttnProblem &a, hipStream_t s) {
     FwdParams p{a.q, a.k, a.v, a.o, a.lse, SeqMap{a.cu, a.n_seqs, a.T}, a.N, a.qs, a.ks, a.vs, a.Hq, a.Hkv,
                 a.Hq / a.Hkv, a.hd, a.scale * kLog2e, (a.N + 127) / 128, false};
     p.order = p.ntiles * p.Hq > device_cus();  // with a block or less per CU all start at once
-    if (a.dtype == Dtype::BF16) dispatch<BF16>(p, s);
+    if (attn_few_rows(p.ntiles * p.Hq, p.seq, p.N)) attn_fwd_short(p, a.dtype, s);
+    else if (a.dtype == Dtype::BF16) dispatch<BF16>(p, s);
     else dispatch<F32>(p, s);
     return hipGetLastError();
 }

@@ -1,0 +1,465 @@
+// attn_short.hip -- the attention of attn_fwd.hip and its gradients
+// (attn_bwd.hip) for inputs of few rows: one short prompt, few heads.
+//
+// Blocks of 128 rows would leave most of the device idle and make every one of
+// them a long chain of tiles.  Here a block takes 32 rows (queries, or keys for
+// dk and dv), and its four waves split the walk over the other axis: tile i of
+// 32 goes to wave i % 4, which loads it into LDS stages of its own (no
+// barriers; two stages where they fit) and works as the long kernels do.  At
+// the end the waves' sums, brought to one maximum in the forward, are added in
+// LDS in a fixed order.  Four times the blocks, a quarter of the chain.
+#include <algorithm>
+
+#include "attn_common.h"
+
+namespace dsc {
+namespace {
+
+// A wave's stage holds two tiles of 32 rows; both stages of four waves have to
+// leave room for the rest.
+template <class E, int HDC>
+struct ShortCfg {
+    static constexpr int kTile = 32 * Tile<E, HDC>::RB;
+    static constexpr int kStages = 4 * 2 * 2 * kTile <= 131072 ? 2 : 1;
+    static constexpr int PER = kTile / 1024;  // load instructions per tile
+    static_assert(2 * kTile >= 32 * HDC * 4, "a wave's sums fit a stage");
+};
+
+// The wave's n tiles, the next one's loads (PER instructions) in flight during
+// the work on each where there are two stages.
+template <int NST, int PER, class Issue, class Work>
+__device__ __forceinline__ void walk(int n, unsigned char *s0, unsigned char *s1, const Issue &issue, const Work &work) {
+    auto read_done = [&]() __attribute__((always_inline)) { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); };
+    if constexpr (NST == 1) {
+        for (int i = 0; i < n; ++i) {
+            issue(i, s0);
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            work(i, s0);
+            read_done();
+        }
+    } else {
+        auto step = [&](int i, unsigned char *cur, unsigned char *other) __attribute__((always_inline)) {
+            if (i + 1 < n) {
+                issue(i + 1, other);
+                asm volatile("s_waitcnt vmcnt(%0)" ::"n"(PER) : "memory");
+            } else {
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            }
+            work(i, cur);
+            read_done();
+        };
+        if (n > 0) issue(0, s0);
+        for (int i = 0; i < n; i += 2) {
+            step(i, s0, s1);
+            if (i + 1 < n) step(i + 1, s1, s0);
+        }
+    }
+}
+
+// A wave's transposed sums (channel, row lane%32) to LDS as (HDC, 32).
+template <int DT>
+__device__ __forceinline__ void park(const floatx16 (&acc)[DT], unsigned char *dst, int lane) {
+    float *p = reinterpret_cast<float *>(dst) + (lane & 31);
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) p[32 * (32 * d + res_row(i, lane >> 5))] = acc[d][i];
+}
+
+// Row r of the block: four channels from d, sum over the waves of w[i] times
+// their parked sums (stage bytes apart), times mul, to memory.
+template <class E>
+__device__ __forceinline__ void join4(const unsigned char *st, int stage, int r, int d, const float (&w)[4], float mul,
+                                      typename E::store_t *dst) {
+    float v[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        float a = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            a = __builtin_fmaf(reinterpret_cast<const float *>(st + i * stage)[32 * (d + c) + r], w[i], a);
+        v[c] = a * mul;
+    }
+    if constexpr (sizeof(typename E::store_t) == 4) *reinterpret_cast<float4 *>(dst) = make_float4(v[0], v[1], v[2], v[3]);
+    else *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+}
+
+// As Tile::add_nonfinite, for four channels of one row.
+template <class E, class Open>
+__device__ void add_nonfinite4(typename E::store_t *dst, const typename E::store_t *src, int64_t stride, int r0, int r1,
+                               const Open &open) {
+    for (int c = 0; c < 4; ++c) {
+        float a = 0.f;
+        bool any = false;
+#pragma clang loop unroll(disable)
+        for (int r = r0; r < r1; ++r) {
+            const float x = load_elem<E>(src + r * stride + c);
+            if ((__float_as_uint(x) & 0x7f800000u) == 0x7f800000u && open(r)) a += x, any = true;
+        }
+        if (!any) continue;
+        a += load_elem<E>(dst + c);
+        if constexpr (sizeof(typename E::store_t) == 4) dst[c] = a;
+        else dst[c] = to_bf16(a);
+    }
+}
+
+// Whether the wave's own tile holds a value that is not finite; zeroed then.
+template <class T>
+__device__ __forceinline__ bool own_dirty(unsigned char *t, int lane) {
+    if (!T::template scan<32, 1>(t, 0, lane)) return false;
+    T::template clean<32, 1>(t, 0, lane);
+    wave_lds_fence();
+    return true;
+}
+
+template <class E, int HDC>
+__global__ __launch_bounds__(256, 1) void attn_fwd_short_kernel(FwdParams p) {
+    using T = Tile<E, HDC>;
+    using M = Mma<E>;
+    using S = typename E::store_t;
+    using frag = typename M::frag;
+    using C = ShortCfg<E, HDC>;
+    constexpr int KF = HDC / M::KC, DT = HDC / 32, PF = 16 / M::PR, SB = 2 * C::kTile;
+    __shared__ __align__(512) unsigned char st0[4 * SB], st1[C::kStages == 2 ? 4 * SB : 16];
+    __shared__ float stat[4][32][2];
+    __shared__ int spoilt;
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
+    const typename T::Lane lofs(lane);
+    const int head = (int)(blockIdx.x % p.Hq), kvh = head % p.Hkv, qh = kvh * p.G + head / p.Hkv;
+    const int64_t m0 = 32 * (p.ntiles - 1 - blockIdx.x / p.Hq), row = m0 + (lane & 31);
+    int64_t start, end;
+    p.seq.find(row < p.N ? row : p.N - 1, start, end);
+    const int kv0 = __builtin_amdgcn_readlane((int)start, 0), last_start = __builtin_amdgcn_readlane((int)start, 31);
+    const int kv_end = (int)min(m0 + 32, p.N), qi = (int)row, lo = (int)start;
+    if (tid == 0) spoilt = 0;
+    __syncthreads();
+
+    const S *kb = static_cast<const S *>(p.k) + (int64_t)kvh * p.hd, *vb = static_cast<const S *>(p.v) + (int64_t)kvh * p.hd;
+    frag qf[KF];
+    T::load_row(qf, static_cast<const S *>(p.q) + (int64_t)qh * p.hd, p.qs, row, p.N, p.hd, lane);
+    floatx16 acc[DT];
+#pragma unroll
+    for (int d = 0; d < DT; ++d) acc[d] = zero16();
+    float mx = -INFINITY, sum = 0.f;
+    auto tile_masked = [&](int n0) { return n0 + 31 > (int)m0 || n0 < last_start; };
+    auto first = [&](int i) { return kv0 + 32 * (wave + 4 * i); };
+
+    const int tiles = (kv_end - kv0 + 31) / 32;
+    walk<C::kStages, 2 * C::PER>(
+        (tiles + 3 - wave) / 4, st0 + wave * SB, st1 + (C::kStages == 2 ? wave * SB : 0),
+        [&](int i, unsigned char *st) __attribute__((always_inline)) {
+            T::template load<32, 1>(st, kb, p.ks, first(i), kv_end, p.hd, 0, lane);
+            T::template load<32, 1>(st + C::kTile, vb, p.vs, first(i), kv_end, p.hd, 0, lane);
+        },
+        [&](int i, unsigned char *ks) __attribute__((always_inline)) {
+            unsigned char *vs = ks + C::kTile;
+            const int n0 = first(i);
+            const bool masked = tile_masked(n0);
+            if (masked && own_dirty<T>(vs, lane)) spoilt = 1;
+            const typename T::Lane ln = lofs.fresh();
+            floatx16 s = zero16();
+#pragma unroll
+            for (int kc = 0; kc < KF; ++kc) s = M::mul(T::read_row(ks, 0, kc, ln), qf[kc], s);
+            if (masked) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int key = n0 + res_row(e, h);
+                    if (key > qi || key < lo) s[e] = -INFINITY;
+                }
+            }
+            float top = s[0];
+#pragma unroll
+            for (int e = 1; e < 16; ++e) top = fmaxf(top, s[e]);
+            top = fmaxf(top, other_half(top));
+            const float nm = fmaxf(mx, top), safe = nm == -INFINITY ? 0.f : nm;
+            const float al = __builtin_amdgcn_exp2f((mx - safe) * p.c2), mc = safe * p.c2;
+            mx = nm;
+            sum *= al;
+#pragma unroll
+            for (int d = 0; d < DT; ++d) acc[d] *= al;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                s[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], p.c2, -mc));
+                sum += s[e];
+            }
+#pragma unroll
+            for (int f = 0; f < PF; ++f) {
+                const frag pf = M::pack(s, f);
+#pragma unroll
+                for (int d = 0; d < DT; ++d) acc[d] = M::mul(T::read_tr(vs, 0, f, d, ln), pf, acc[d]);
+            }
+        });
+
+    sum += other_half(sum);
+    park(acc, st0 + wave * SB, lane);
+    if (h == 0) stat[wave][lane][0] = mx, stat[wave][lane][1] = sum;
+    __syncthreads();
+    const int r = tid & 31, part = tid >> 5;
+    if (m0 + r >= p.N) return;
+    float m = -INFINITY, w[4], l = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = fmaxf(m, stat[i][r][0]);
+    const float safe = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w[i] = __builtin_amdgcn_exp2f((stat[i][r][0] - safe) * p.c2);
+        l = __builtin_fmaf(stat[i][r][1], w[i], l);
+    }
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // NaN stays
+    int64_t rs, re;
+    p.seq.find(m0 + r, rs, re);
+#pragma unroll
+    for (int j = 0; j < HDC / 32; ++j) {
+        const int d = part * (HDC / 8) + 4 * j;
+        if (d >= p.hd) continue;
+        S *o = static_cast<S *>(p.o) + ((m0 + r) * p.Hq + qh) * p.hd + d;
+        join4<E>(st0, SB, r, d, w, inv, o);
+        if (__builtin_expect(spoilt, 0))
+            add_nonfinite4<E>(o, vb + d, p.vs, kv0, kv_end, [&](int t) {
+                return t <= (int)m0 + r && t >= rs && tile_masked(t - (t - kv0) % 32);
+            });
+    }
+    if (p.lse && part == 0) p.lse[(int64_t)qh * p.N + m0 + r] = m * p.c2 * kLn2 + __logf(l);
+}
+
+template <class E, int HDC>
+__global__ __launch_bounds__(256, 1) void attn_dq_short_kernel(BwdParams p) {
+    using T = Tile<E, HDC>;
+    using M = Mma<E>;
+    using S = typename E::store_t;
+    using frag = typename M::frag;
+    using C = ShortCfg<E, HDC>;
+    constexpr int KF = HDC / M::KC, DT = HDC / 32, PF = 16 / M::PR, SB = 2 * C::kTile;
+    __shared__ __align__(512) unsigned char st0[4 * SB], st1[C::kStages == 2 ? 4 * SB : 16];
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
+    const typename T::Lane lofs(lane);
+    const int head = (int)(blockIdx.x % p.Hq), kvh = head % p.Hkv, qh = kvh * p.G + head / p.Hkv;
+    const int64_t m0 = 32 * (p.ntiles - 1 - blockIdx.x / p.Hq), row = m0 + (lane & 31);
+    int64_t start, end;
+    p.seq.find(row < p.N ? row : p.N - 1, start, end);
+    const int kv0 = __builtin_amdgcn_readlane((int)start, 0), last_start = __builtin_amdgcn_readlane((int)start, 31);
+    const int kv_end = (int)min(m0 + 32, p.N), qi = (int)row, lo = (int)start;
+
+    const S *kb = static_cast<const S *>(p.k) + (int64_t)kvh * p.hd, *vb = static_cast<const S *>(p.v) + (int64_t)kvh * p.hd;
+    const int64_t os = (int64_t)p.Hq * p.hd;
+    frag qf[KF], gf[KF];
+    T::load_row(qf, static_cast<const S *>(p.q) + (int64_t)qh * p.hd, p.qs, row, p.N, p.hd, lane);
+    T::load_row(gf, static_cast<const S *>(p.dout) + (int64_t)qh * p.hd, os, row, p.N, p.hd, lane);
+    const float delta = row_delta<T>(gf, static_cast<const S *>(p.o) + (int64_t)qh * p.hd, os, row, p.N, p.hd, lane);
+    const float lse2 = row < p.N ? p.lse[(int64_t)qh * p.N + row] * kLog2e : 0.f;
+    if (wave == 0 && h == 0 && row < p.N) {
+        p.delta[(int64_t)qh * p.N + row] = delta;
+        p.lse2[(int64_t)qh * p.N + row] = lse2;
+    }
+    floatx16 acc[DT];
+#pragma unroll
+    for (int d = 0; d < DT; ++d) acc[d] = zero16();
+    auto first = [&](int i) { return kv0 + 32 * (wave + 4 * i); };
+
+    const int tiles = (kv_end - kv0 + 31) / 32;
+    walk<C::kStages, 2 * C::PER>(
+        (tiles + 3 - wave) / 4, st0 + wave * SB, st1 + (C::kStages == 2 ? wave * SB : 0),
+        [&](int i, unsigned char *st) __attribute__((always_inline)) {
+            T::template load<32, 1>(st, kb, p.ks, first(i), kv_end, p.hd, 0, lane);
+            T::template load<32, 1>(st + C::kTile, vb, p.vs, first(i), kv_end, p.hd, 0, lane);
+        },
+        [&](int i, unsigned char *ks) __attribute__((always_inline)) {
+            const int n0 = first(i);
+            const bool masked = n0 + 31 > (int)m0 || n0 < last_start;
+            const typename T::Lane ln = lofs.fresh();
+            floatx16 s = zero16(), dp = zero16();
+#pragma unroll
+            for (int kc = 0; kc < KF; ++kc) s = M::mul(T::read_row(ks, 0, kc, ln), qf[kc], s);
+#pragma unroll
+            for (int kc = 0; kc < KF; ++kc) dp = M::mul(T::read_row(ks + C::kTile, 0, kc, ln), gf[kc], dp);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                s[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], p.c2, -lse2)) * (dp[e] - delta);
+            if (masked) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int key = n0 + res_row(e, h);
+                    if (key > qi || key < lo) s[e] = 0.f;
+                }
+                wave_lds_fence();
+                own_dirty<T>(ks, lane);  // rows that see such a key have NaN in ds already
+            }
+#pragma unroll
+            for (int f = 0; f < PF; ++f) {
+                const frag df = M::pack(s, f);
+#pragma unroll
+                for (int d = 0; d < DT; ++d) acc[d] = M::mul(T::read_tr(ks, 0, f, d, ln), df, acc[d]);
+            }
+        });
+
+    park(acc, st0 + wave * SB, lane);
+    __syncthreads();
+    const int r = tid & 31, part = tid >> 5;
+    if (m0 + r >= p.N) return;
+    const float w[4] = {1.f, 1.f, 1.f, 1.f};
+#pragma unroll
+    for (int j = 0; j < HDC / 32; ++j) {
+        const int d = part * (HDC / 8) + 4 * j;
+        if (d < p.hd)
+            join4<E>(st0, SB, r, d, w, p.scale, static_cast<S *>(p.dq) + (m0 + r) * p.dqs + (int64_t)qh * p.hd + d);
+    }
+}
+
+template <class E, int HDC>
+__global__ __launch_bounds__(256, 1) void attn_dkv_short_kernel(BwdParams p) {
+    using T = Tile<E, HDC>;
+    using M = Mma<E>;
+    using S = typename E::store_t;
+    using frag = typename M::frag;
+    using C = ShortCfg<E, HDC>;
+    // a stage: Q tile, dout tile, then lse2 and delta of the rows (64 places each)
+    constexpr int KF = HDC / M::KC, DT = HDC / 32, PF = 16 / M::PR, LO = 2 * C::kTile, DO = LO + 256, SB = LO + 512;
+    __shared__ __align__(512) unsigned char st0[4 * SB], st1[C::kStages == 2 ? 4 * SB : 16];
+    __shared__ int spoilt;
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
+    const typename T::Lane lofs(lane);
+    const int kvh = (int)(blockIdx.x % p.Hkv);
+    const int64_t n0 = 32 * (int64_t)(blockIdx.x / p.Hkv), key = n0 + (lane & 31);
+    int64_t start, end;
+    p.seq.find(key < p.N ? key : p.N - 1, start, end);
+    const int first_end = __builtin_amdgcn_readlane((int)end, 0), q_end = __builtin_amdgcn_readlane((int)end, 31);
+    const int q0 = (int)n0, ki = (int)key, hi = (int)end;
+    if (tid == 0) spoilt = 0;
+    __syncthreads();
+
+    const int64_t os = (int64_t)p.Hq * p.hd;
+    frag kf[KF], vf[KF];
+    T::load_row(kf, static_cast<const S *>(p.k) + (int64_t)kvh * p.hd, p.ks, key, p.N, p.hd, lane);
+    T::load_row(vf, static_cast<const S *>(p.v) + (int64_t)kvh * p.hd, p.vs, key, p.N, p.hd, lane);
+    floatx16 dk[DT], dv[DT];
+#pragma unroll
+    for (int d = 0; d < DT; ++d) dk[d] = zero16(), dv[d] = zero16();
+    const int nt = (q_end - q0 + 31) / 32, total = nt * p.G;
+    auto tile_masked = [&](int m0) { return m0 < (int)n0 + 31 || m0 + 32 > first_end; };
+
+    walk<C::kStages, 2 * C::PER + 2>(
+        (total + 3 - wave) / 4, st0 + wave * SB, st1 + (C::kStages == 2 ? wave * SB : 0),
+        [&](int i, unsigned char *st) __attribute__((always_inline)) {
+            const int it = wave + 4 * i, g = it / nt, m0 = q0 + (it - g * nt) * 32;
+            const int64_t qh = (int64_t)kvh * p.G + g;
+            T::template load<32, 1>(st, static_cast<const S *>(p.q) + qh * p.hd, p.qs, m0, q_end, p.hd, 0, lane);
+            T::template load<32, 1>(st + C::kTile, static_cast<const S *>(p.dout) + qh * p.hd, os, m0, q_end, p.hd, 0, lane);
+            const int64_t at = qh * p.N + m0, bytes = 4 * (int64_t)min(32, q_end - m0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(make_stream(p.lse2 + at, bytes), (attn_lds_void *)(st + LO), 4, 4u * lane, 0, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(make_stream(p.delta + at, bytes), (attn_lds_void *)(st + DO), 4, 4u * lane, 0, 0, 0);
+        },
+        [&](int i, unsigned char *qt) __attribute__((always_inline)) {
+            unsigned char *gt = qt + C::kTile;
+            const int it = wave + 4 * i, g = it / nt, m0 = q0 + (it - g * nt) * 32;
+            const float *lt = reinterpret_cast<const float *>(qt + LO), *dt = reinterpret_cast<const float *>(qt + DO);
+            const bool masked = tile_masked(m0);
+            if (masked) {
+                const bool a = own_dirty<T>(qt, lane), b = own_dirty<T>(gt, lane);
+                if (a || b) spoilt = 1;
+            }
+            const typename T::Lane ln = lofs.fresh();
+            floatx16 s = zero16(), dp = zero16();
+#pragma unroll
+            for (int kc = 0; kc < KF; ++kc) s = M::mul(T::read_row(qt, 0, kc, ln), kf[kc], s);
+#pragma unroll
+            for (int kc = 0; kc < KF; ++kc) dp = M::mul(T::read_row(gt, 0, kc, ln), vf[kc], dp);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                s[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], p.c2, -lt[res_row(e, h)]));
+                dp[e] = s[e] * (dp[e] - dt[res_row(e, h)]);
+            }
+            if (masked) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int qr = m0 + res_row(e, h);
+                    if (qr < ki || qr >= hi) s[e] = 0.f, dp[e] = 0.f;
+                }
+            }
+#pragma unroll
+            for (int f = 0; f < PF; ++f) {
+                const frag pf = M::pack(s, f), df = M::pack(dp, f);
+#pragma unroll
+                for (int d = 0; d < DT; ++d) {
+                    dv[d] = M::mul(T::read_tr(gt, 0, f, d, ln), pf, dv[d]);
+                    dk[d] = M::mul(T::read_tr(qt, 0, f, d, ln), df, dk[d]);
+                }
+            }
+        });
+
+    // dk to the first stage, dv to the second (or to the second half of a single one)
+    unsigned char *const vst = C::kStages == 2 ? st1 : st0 + C::kTile;
+    static_assert(C::kStages == 2 || C::kTile >= 32 * HDC * 4, "both sums fit a single stage");
+    park(dk, st0 + wave * SB, lane);
+    park(dv, vst + wave * SB, lane);
+    __syncthreads();
+    const int r = tid & 31, part = tid >> 5;
+    if (n0 + r >= p.N) return;
+    int64_t rs, re;
+    p.seq.find(n0 + r, rs, re);
+    const float w[4] = {1.f, 1.f, 1.f, 1.f};
+#pragma unroll
+    for (int j = 0; j < HDC / 32; ++j) {
+        const int d = part * (HDC / 8) + 4 * j;
+        if (d >= p.hd) continue;
+        S *dvp = static_cast<S *>(p.dv) + (n0 + r) * p.dvs + (int64_t)kvh * p.hd + d;
+        join4<E>(st0, SB, r, d, w, p.scale, static_cast<S *>(p.dk) + (n0 + r) * p.dks + (int64_t)kvh * p.hd + d);
+        join4<E>(vst, SB, r, d, w, 1.f, dvp);
+        if (__builtin_expect(spoilt, 0))
+            for (int g = 0; g < p.G; ++g)
+                add_nonfinite4<E>(dvp, static_cast<const S *>(p.dout) + ((int64_t)kvh * p.G + g) * p.hd + d, os, q0, q_end,
+                                  [&](int t) { return t >= (int)n0 + r && t < re && tile_masked(t - (t - q0) % 32); });
+    }
+}
+
+// One launch of KERNEL<E, HDC> with a block per 32 rows and head.
+#define DSC_ATTN_SHORT(KERNEL, P, HEADS)                                                             \
+    do {                                                                                               \
+        const dim3 grid((unsigned)((P).ntiles * (HEADS))), block(256);                                 \
+        if ((P).hd <= 64) hipLaunchKernelGGL((KERNEL<E, 64>), grid, block, 0, s, P);                   \
+        else if ((P).hd <= 96) hipLaunchKernelGGL((KERNEL<E, 96>), grid, block, 0, s, P);              \
+        else hipLaunchKernelGGL((KERNEL<E, 128>), grid, block, 0, s, P);                               \
+    } while (0)
+
+template <class E>
+void fwd(const FwdParams &p, hipStream_t s) { DSC_ATTN_SHORT(attn_fwd_short_kernel, p, p.Hq); }
+template <class E>
+void dq(const BwdParams &p, hipStream_t s) { DSC_ATTN_SHORT(attn_dq_short_kernel, p, p.Hq); }
+template <class E>
+void dkv(const BwdParams &p, hipStream_t s) { DSC_ATTN_SHORT(attn_dkv_short_kernel, p, p.Hkv); }
+
+}  // namespace
+
+// Half a block of 128 rows per CU or fewer always run short; up to three
+// quarters with sequences of 512 tokens or more on average, up to one with
+// 2048 or more, where the long kernels' chains grow faster than the short
+// ones' extra LDS traffic (forward, long / short kernels, us: 8 x 256 tokens,
+// 12 heads of 64, 192 blocks 9.4 / 11.8; 2 x 512, 24 heads, 192 blocks
+// 12.8 / 11.9; 2048, 12 heads, 192 blocks 35 / 21; 2048, 16 heads, 256 blocks
+// 34 / 25; 4 x 512, 16 heads of 128, 256 blocks 19 / 27).
+bool attn_few_rows(int64_t blocks, const SeqMap &seq, int64_t N) {
+    const int64_t cus = device_cus(), mean = seq.cu ? N / std::max(seq.n_seqs, 1) : seq.T;
+    return 4 * blocks <= cus * (mean >= 2048 ? 4 : mean >= 512 ? 3 : 2);
+}
+
+void attn_fwd_short(FwdParams p, Dtype dt, hipStream_t s) {
+    p.ntiles = (p.N + 31) / 32;
+    if (dt == Dtype::BF16) fwd<BF16>(p, s);
+    else fwd<F32>(p, s);
+}
+
+void attn_dq_short(BwdParams p, Dtype dt, hipStream_t s) {
+    p.ntiles = (p.N + 31) / 32;
+    if (dt == Dtype::BF16) dq<BF16>(p, s);
+    else dq<F32>(p, s);
+}
+
+void attn_dkv_short(BwdParams p, Dtype dt, hipStream_t s) {
+    p.ntiles = (p.N + 31) / 32;
+    if (dt == Dtype::BF16) dkv<BF16>(p, s);
+    else dkv<F32>(p, s);
+}
+
+}  // namespace dsc

@@ -92,6 +92,14 @@ PROMPTS = [
     ("fp32", 2, 160, 4, 1, 128, [33, 255, 32], "dense"),
     ("fp32", 1, 257, 2, 2, 12, None, "packed"),
     ("fp32", 1, 130, 5, 1, 100, [64, 66], "packed"),
+    # enough blocks of 128 rows for the kernels for long inputs (forward, dq; with Hkv blocks dk and dv too)
+    ("bf16", 8, 128, 40, 40, 64, None, "packed"),
+    ("bf16", 1, 1100, 40, 20, 128, [1, 1, 31, 32, 33, 0, 64, 65, 73, 300, 500], "packed"),
+    ("bf16", 3, 333, 48, 24, 80, [250, 249, 1, 499], "dense"),
+    ("bf16", 1, 1031, 30, 30, 96, [57] * 18 + [5], "packed"),
+    ("fp32", 4, 160, 52, 26, 64, None, "packed"),
+    ("fp32", 1, 901, 34, 34, 100, [1, 130, 2, 168, 600], "packed"),
+    ("fp32", 1, 650, 44, 44, 128, [33, 255, 32, 330], "dense"),
 ]
 
 
@@ -145,14 +153,15 @@ def test_gradients_against_differences():
         assert abs(num - float(np.sum(flat64(got[n]) * u))) <= float(np.sum(bounds[n][1] * np.abs(u))) + 1e-5
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(4, 2), (80, 80)])  # few rows, and the kernels for long inputs
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
-def test_what_a_row_must_not_see(dtype, bad):
+def test_what_a_row_must_not_see(dtype, bad, Hq, Hkv):
     """A token of non-finite q, k, v and g changes neither earlier rows of its sequence nor other sequences."""
     lens, at = [50, 70, 100], 50 + 33
     scale = 0.125
-    row, q, k, v = qkv(1, 220, 4, 2, 64, dtype, 31)
-    g = torch.from_numpy(np.random.default_rng(8).standard_normal((1, 220, 4, 64), dtype=np.float32)).to(q.dtype).cuda()
+    row, q, k, v = qkv(1, 220, Hq, Hkv, 64, dtype, 31)
+    g = torch.from_numpy(np.random.default_rng(8).standard_normal((1, 220, Hq, 64), dtype=np.float32)).to(q.dtype).cuda()
     clean = run(q, k, v, g, cu_of(lens), scale)
     clean = {n: t.clone() for n, t in clean.items()}
     row[0, at] = bad
@@ -167,13 +176,14 @@ def test_what_a_row_must_not_see(dtype, bad):
     assert torch.equal(got["dq"][0, 50:at], clean["dq"][0, 50:at])
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(4, 2), (160, 80)])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("bad", [float("nan"), float("-inf")])
-def test_gradient_rows_that_a_key_must_not_see(dtype, bad):
+def test_gradient_rows_that_a_key_must_not_see(dtype, bad, Hq, Hkv):
     """One token's dL/do not finite: only its own dq, and dk, dv of the keys that it sees."""
     at = 50 + 33
-    _, q, k, v = qkv(1, 220, 4, 2, 64, dtype, 33)
-    g = torch.from_numpy(np.random.default_rng(9).standard_normal((1, 220, 4, 64), dtype=np.float32)).to(q.dtype).cuda()
+    _, q, k, v = qkv(1, 220, Hq, Hkv, 64, dtype, 33)
+    g = torch.from_numpy(np.random.default_rng(9).standard_normal((1, 220, Hq, 64), dtype=np.float32)).to(q.dtype).cuda()
     cu = cu_of([50, 70, 100])
     clean = {n: t.clone() for n, t in run(q, k, v, g, cu, 0.125).items()}
     g[0, at, 1, 3] = bad  # one channel of one head (of key head 0)
@@ -189,9 +199,10 @@ def test_gradient_rows_that_a_key_must_not_see(dtype, bad):
     assert torch.equal(got["dq"][0, at, 0], clean["dq"][0, at, 0]) and not torch.isfinite(got["dq"][0, at, 1]).any()
 
 
-def test_same_bits_every_time():
-    _, q, k, v = qkv(2, 400, 8, 2, 128, "bf16", 41)
-    g = torch.randn(2, 400, 8, 128, device="cuda").to(q.dtype)
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (64, 32)])
+def test_same_bits_every_time(Hq, Hkv):
+    _, q, k, v = qkv(2, 400, Hq, Hkv, 128, "bf16", 41)
+    g = torch.randn(2, 400, Hq, 128, device="cuda").to(q.dtype)
     a = {n: t.clone() for n, t in run(q, k, v, g, None, 0.1).items()}
     for _ in range(3):
         b = run(q, k, v, g, None, 0.1)
