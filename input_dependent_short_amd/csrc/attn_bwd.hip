@@ -23,7 +23,7 @@ constexpr int kBT = sizeof(typename E::store_t) == 2 ? 64 : 32;  // rows per wal
 
 
 template <class E, int HDC>
-__global__ __launch_bounds__(256, sizeof(typename E::store_t) == 2 ? 2 : 1) void attn_dq_kernel(BwdParams p) {
+__global__ __launch_bounds__(256, (sizeof(typename E::store_t) == 2 ? 2 : 1)) void attn_dq_kernel(BwdParams p) {
     using T = Tile<E, HDC>;
     using M = Mma<E>;
     using S = typename E::store_t;
@@ -34,20 +34,23 @@ __global__ __launch_bounds__(256, sizeof(typename E::store_t) == 2 ? 2 : 1) void
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
     const typename T::Lane lofs(lane);
+    __shared__ int32_t cu_lds[kSeqLds];
+    const Seqs seq(p.seq, cu_lds, tid, 256);
+    __syncthreads();
     const int head = (int)(blockIdx.x % p.Hq), kvh = head % p.Hkv, qh = kvh * p.G + head / p.Hkv;
-    const int64_t tile = heavy_tile<false>(p.seq, p.N, p.ntiles, blockIdx.x / p.Hq, p.order, reinterpret_cast<int *>(k0s), tid);
+    const int64_t tile = heavy_tile<false>(seq, (int)p.N, (int)p.ntiles, blockIdx.x / p.Hq, p.order, reinterpret_cast<int *>(k0s), tid);
     const int64_t m0 = tile * BM, w0 = m0 + 32 * wave, row = w0 + (lane & 31);
 
-    int64_t start, blk_start, end;
-    p.seq.find((m0 + BM < p.N ? m0 + BM : p.N) - 1, start, end);
+    int start, blk_start, end;
+    seq.find_uniform((int)(m0 + BM < p.N ? m0 + BM : p.N) - 1, start, end);
     const int blk_last_start = (int)start;
-    p.seq.find(m0, blk_start, end);
+    seq.find_uniform((int)m0, blk_start, end);
     if (tid == 0) flag = -1;
-    p.seq.find(row < p.N ? row : p.N - 1, start, end);
+    seq.find((int)min(row, p.N - 1), start, end);
     const int kv0 = (int)blk_start, kv_end = (int)min(m0 + BM, p.N);
     const int wlast = (int)min(w0 + 31, p.N - 1);
-    const int wfirst_key = __builtin_amdgcn_readlane((int)start, 0);
-    const int wlast_start = __builtin_amdgcn_readlane((int)start, 31);
+    const int wfirst_key = __builtin_amdgcn_readlane(start, 0);
+    const int wlast_start = __builtin_amdgcn_readlane(start, 31);
     const int qi = (int)row, lo = (int)start;
 
     const S *kb = static_cast<const S *>(p.k) + (int64_t)kvh * p.hd;
@@ -164,20 +167,23 @@ __global__ __launch_bounds__((64 * DkvCfg<E, HDC>::NW), (DkvCfg<E, HDC>::kOcc)) 
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
     const typename T::Lane lofs(lane);
+    __shared__ int32_t cu_lds[kSeqLds];
+    const Seqs seq(p.seq, cu_lds, tid, 256);
+    __syncthreads();
     const int kvh = (int)(blockIdx.x % p.Hkv);
-    const int64_t tile = heavy_tile<true>(p.seq, p.N, p.ntiles, blockIdx.x / p.Hkv, p.order, reinterpret_cast<int *>(st0), tid);
+    const int64_t tile = heavy_tile<true>(seq, (int)p.N, (int)p.ntiles, blockIdx.x / p.Hkv, p.order, reinterpret_cast<int *>(st0), tid);
     const int64_t n0b = tile * BK, w0 = n0b + 32 * wave, key = w0 + (lane & 31);
 
-    int64_t start, end, blk_end;
+    int start, end, blk_end;
     const int64_t blk_last = min(n0b + BK, p.N) - 1;
-    p.seq.find(n0b, start, end);
+    seq.find_uniform((int)n0b, start, end);
     const int blk_first_end = (int)end;
-    p.seq.find(blk_last, start, blk_end);
+    seq.find_uniform((int)blk_last, start, blk_end);
     if (tid == 0) flag = -1;
-    p.seq.find(key < p.N ? key : p.N - 1, start, end);
+    seq.find((int)min(key, p.N - 1), start, end);
     const int q_end = (int)blk_end, q0 = (int)n0b;
-    const int wfirst_end = __builtin_amdgcn_readlane((int)end, 0);   // rows below it see the wave's first key
-    const int wlast_end = __builtin_amdgcn_readlane((int)end, 31);  // rows at or past it see no key of the wave
+    const int wfirst_end = __builtin_amdgcn_readlane(end, 0);   // rows below it see the wave's first key
+    const int wlast_end = __builtin_amdgcn_readlane(end, 31);  // rows at or past it see no key of the wave
     const int ki = (int)key, hi = (int)end;
 
     auto phase = [&]() __attribute__((always_inline)) {

@@ -222,22 +222,22 @@ struct Tile {
                                                          const Open &open) {
         if (row >= N) return;
 #pragma clang loop unroll(disable)
-        for (int d = 4 * (lane >> 5); d < hd; d += 8) {
+        for (int d = VEC * (lane >> 5); d < hd; d += 2 * VEC) {
             S *o = dst + row * dstride + d;
-            float a[4] = {0.f, 0.f, 0.f, 0.f};
+            float a[VEC] = {};
             bool any = false;
 #pragma clang loop unroll(disable)
             for (int r = r0; r < r1; ++r) {
                 if (!open(r)) continue;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < VEC; ++i) {
                     const float x = load_elem<E>(src + r * stride + d + i);
                     if ((__float_as_uint(x) & 0x7f800000u) == 0x7f800000u) a[i] += x, any = true;
                 }
             }
             if (!any) continue;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < VEC; ++i) {
                 const float v = load_elem<E>(o + i) + a[i];
                 if constexpr (sizeof(S) == 4) o[i] = v;
                 else o[i] = to_bf16(v);
@@ -259,24 +259,41 @@ struct Tile {
     }
 
     // A transposed result (channel 32*dt + res_row(i, h), token row lane%32)
-    // to the token's row in memory, four channels at a time.
+    // to the token's row in memory, 16 bytes at a time: bf16 halves exchange
+    // runs of four channels first, so that each lane holds eight in a row (a
+    // head has a multiple of eight).
     __device__ __forceinline__ static void store_row(const floatx16 (&r)[HDC / 32], float mul, S *base, int64_t stride,
                                                      int64_t row, int64_t N, int hd, int lane) {
-        if (row >= N) return;
-        S *p = base + row * stride + 4 * (lane >> 5);
+        const int h = lane >> 5;
+        const bool in = row < N;
+        S *p = base + row * stride;
 #pragma unroll
-        for (int dt = 0; dt < HDC / 32; ++dt)
+        for (int dt = 0; dt < HDC / 32; ++dt) {
+            if constexpr (sizeof(S) == 4) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int d = 32 * dt + 8 * q;
-                if (d + 4 * (lane >> 5) >= hd) continue;
-                const float a = r[dt][4 * q] * mul, b = r[dt][4 * q + 1] * mul, c = r[dt][4 * q + 2] * mul,
-                            e = r[dt][4 * q + 3] * mul;
-                if constexpr (sizeof(S) == 4)
-                    *reinterpret_cast<float4 *>(p + d) = make_float4(a, b, c, e);
-                else
-                    *reinterpret_cast<uint2 *>(p + d) = make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, e));
+                for (int q = 0; q < 4; ++q) {
+                    const int d = 32 * dt + 8 * q + 4 * h;
+                    if (in && d < hd)
+                        *reinterpret_cast<float4 *>(p + d) = make_float4(r[dt][4 * q] * mul, r[dt][4 * q + 1] * mul,
+                                                                         r[dt][4 * q + 2] * mul, r[dt][4 * q + 3] * mul);
+                }
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; q += 2) {
+                    uint32_t w[2][2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            w[e][i] = pack_bf16x2(r[dt][4 * (q + e) + 2 * i] * mul, r[dt][4 * (q + e) + 2 * i + 1] * mul);
+                    // the high half's run q against the low half's run q+1
+                    const auto x = __builtin_amdgcn_permlane32_swap(w[0][0], w[1][0], false, false);
+                    const auto y = __builtin_amdgcn_permlane32_swap(w[0][1], w[1][1], false, false);
+                    const int d = 32 * dt + 8 * (q + h);
+                    if (in && d < hd) *reinterpret_cast<uint4 *>(p + d) = make_uint4(x[0], y[0], x[1], y[1]);
+                }
             }
+        }
     }
 };
 
@@ -310,6 +327,55 @@ __device__ __forceinline__ bool tile_dirty(unsigned char *a, unsigned char *b, i
     return dirty;
 }
 
+// The sequences, for a block that looks up several tokens: the offsets are
+// copied to LDS once (up to kSeqLds of them), so a search costs LDS steps
+// instead of a chain of dependent memory loads, and positions are 32 bits wide
+// (B*T < 2^31).
+constexpr int kSeqLds = 512;
+struct Seqs {
+    const int32_t *lds, *cu;
+    int32_t n;
+    uint32_t T;
+    // Every thread of the block calls this, before a barrier.
+    __device__ __forceinline__ Seqs(const SeqMap &m, int32_t *buf, int tid, int threads)
+        : lds(buf), cu(m.cu), n(m.n_seqs), T((uint32_t)m.T) {
+        if (cu != nullptr && n < kSeqLds)
+            for (int i = tid; i <= n; i += threads) buf[i] = cu[i];
+    }
+    // First token and end of the sequence of a token that every lane agrees on,
+    // in scalar registers (loads through resources in vector registers would
+    // each become a loop).
+    __device__ __forceinline__ void find_uniform(int t, int &start, int &end) const {
+        find(t, start, end);
+        start = __builtin_amdgcn_readfirstlane(start);
+        end = __builtin_amdgcn_readfirstlane(end);
+    }
+    // First token and end of token t's sequence.
+    __device__ __forceinline__ void find(int t, int &start, int &end) const {
+        if (cu == nullptr) {
+            start = (int)((uint32_t)t / T * T);
+            end = start + (int)T;
+            return;
+        }
+        int lo = 0, hi = n;  // cu[lo] <= t < cu[hi]
+        if (n < kSeqLds) {
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (lds[mid] <= t) lo = mid;
+                else hi = mid;
+            }
+            start = lds[lo], end = lds[lo + 1];
+        } else {
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (cu[mid] <= t) lo = mid;
+                else hi = mid;
+            }
+            start = cu[lo], end = cu[lo + 1];
+        }
+    }
+};
+
 // Tile of 128 token rows that a block takes as number `rank` of its head.
 // Tiles differ in work (the rows before them in their sequence, or after them
 // with KEYS), and blocks start in grid order, so the heaviest tiles go first
@@ -321,14 +387,12 @@ __device__ __forceinline__ bool tile_dirty(unsigned char *a, unsigned char *b, i
 // a tile of its own, whatever the weights.  Ends with a barrier.
 constexpr int kRankTiles = 1024, kRankInts = 256 + 4 + 16;
 template <bool KEYS>
-__device__ __forceinline__ int heavy_tile(const SeqMap &seq, int64_t N, int64_t ntiles, int64_t rank, bool order, int *lds,
-                                          int tid) {
-    if (!order) return (int)(KEYS ? rank : ntiles - 1 - rank);
-    if (seq.cu == nullptr && seq.T % 128 == 0) {
-        const int64_t per = seq.T / 128, rows = N / seq.T, at = rank / rows;
-        return (int)((rank % rows) * per + (KEYS ? at : per - 1 - at));
+__device__ __forceinline__ int heavy_tile(const Seqs &seq, int N, int ntiles, int rank, bool order, int *lds, int tid) {
+    if (order && seq.cu == nullptr && seq.T % 128 == 0) {
+        const uint32_t per = seq.T / 128, rows = (uint32_t)N / seq.T, at = (uint32_t)rank / rows;
+        return (int)(((uint32_t)rank - at * rows) * per + (KEYS ? at : per - 1 - at));
     }
-    if (ntiles > kRankTiles) return (int)(KEYS ? rank : ntiles - 1 - rank);
+    if (!order || ntiles > kRankTiles) return KEYS ? rank : ntiles - 1 - rank;
     const int lane = tid & 63, wave = tid >> 6;
     lds[tid] = 0;
     __syncthreads();
@@ -338,10 +402,10 @@ __device__ __forceinline__ int heavy_tile(const SeqMap &seq, int64_t N, int64_t 
         const int t = 256 * c + tid;
         w[c] = -1;
         if (t < ntiles) {
-            int64_t a, b;
-            const int64_t m0 = 128 * (int64_t)t, last = min(m0 + 128, N) - 1;
+            int a, b;
+            const int m0 = 128 * t, last = min(m0 + 128, N) - 1;
             seq.find(KEYS ? last : m0, a, b);
-            w[c] = (int)min((int64_t)255, (KEYS ? b - m0 : last - a) / 128);
+            w[c] = min(255, (KEYS ? b - m0 : last - a) / 128);
             atomicAdd(&lds[w[c]], 1);
         }
     }
@@ -358,7 +422,7 @@ __device__ __forceinline__ int heavy_tile(const SeqMap &seq, int64_t N, int64_t 
         }
         before = upto - n;
         if (before <= rank && rank < upto) {
-            int left = (int)rank - before, b = 255 - 4 * lane;
+            int left = rank - before, b = 255 - 4 * lane;
             while (left >= lds[b]) left -= lds[b--];
             lds[256] = b;
             lds[257] = left;

@@ -28,7 +28,7 @@ template <int HDC>
 constexpr bool kTwoK = HDC <= 64;
 
 template <class E, int HDC>
-__global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdParams p) {
+__global__ __launch_bounds__(256, (sizeof(typename E::store_t) == 4 ? 2 : kTwoK<HDC> ? 4 : 3)) void attn_fwd_kernel(FwdParams p) {
     using T = Tile<E, HDC>;
     using M = Mma<E>;
     using S = typename E::store_t;
@@ -40,24 +40,27 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdParams p) {
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
     const typename T::Lane lofs(lane);
+    __shared__ int32_t cu_lds[kSeqLds];
+    const Seqs seq(p.seq, cu_lds, tid, 256);
+    __syncthreads();
     // Key head fastest: blocks b, b + 8, ... share an XCD, so with a multiple
     // of eight key heads each one's keys and values stay in one XCD's L2.
     const int head = (int)(blockIdx.x % p.Hq), kvh = head % p.Hkv, qh = kvh * p.G + head / p.Hkv;
-    const int64_t tile = heavy_tile<false>(p.seq, p.N, p.ntiles, blockIdx.x / p.Hq, p.order, reinterpret_cast<int *>(k0s), tid);
+    const int64_t tile = heavy_tile<false>(seq, (int)p.N, (int)p.ntiles, blockIdx.x / p.Hq, p.order, reinterpret_cast<int *>(k0s), tid);
     const int64_t m0 = tile * BM, w0 = m0 + 32 * wave, row = w0 + (lane & 31);
 
     // sequence starts: the block's first row, this lane's row, the wave's last row
-    int64_t start, blk_start, end;
-    p.seq.find((m0 + BM < p.N ? m0 + BM : p.N) - 1, start, end);
+    int start, blk_start, end;
+    seq.find_uniform((int)(m0 + BM < p.N ? m0 + BM : p.N) - 1, start, end);
     const int blk_last_start = (int)start;
-    p.seq.find(m0, blk_start, end);
+    seq.find_uniform((int)m0, blk_start, end);
     if (tid == 0) flag = -1;
-    p.seq.find(row < p.N ? row : p.N - 1, start, end);
+    seq.find((int)min(row, p.N - 1), start, end);
     const int kv0 = (int)blk_start;
     const int kv_end = (int)min(m0 + BM, p.N);
     const int wlast = (int)min(w0 + 31, p.N - 1);
-    const int wfirst_key = __builtin_amdgcn_readlane((int)start, 0);   // the wave needs keys from here
-    const int wlast_start = __builtin_amdgcn_readlane((int)start, 31); // every row is open from here
+    const int wfirst_key = __builtin_amdgcn_readlane(start, 0);   // the wave needs keys from here
+    const int wlast_start = __builtin_amdgcn_readlane(start, 31); // every row is open from here
     const int qi = (int)row, lo = (int)start;
 
     const S *kb = static_cast<const S *>(p.k) + (int64_t)kvh * p.hd;

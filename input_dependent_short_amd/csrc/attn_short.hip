@@ -126,11 +126,14 @@ __global__ __launch_bounds__(256, 1) void attn_fwd_short_kernel(FwdParams p) {
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
     const typename T::Lane lofs(lane);
+    __shared__ int32_t cu_lds[kSeqLds];
+    const Seqs seq(p.seq, cu_lds, tid, 256);
+    __syncthreads();
     const int head = (int)(blockIdx.x % p.Hq), kvh = head % p.Hkv, qh = kvh * p.G + head / p.Hkv;
     const int64_t m0 = 32 * (p.ntiles - 1 - blockIdx.x / p.Hq), row = m0 + (lane & 31);
-    int64_t start, end;
-    p.seq.find(row < p.N ? row : p.N - 1, start, end);
-    const int kv0 = __builtin_amdgcn_readlane((int)start, 0), last_start = __builtin_amdgcn_readlane((int)start, 31);
+    int start, end;
+    seq.find((int)min(row, p.N - 1), start, end);
+    const int kv0 = __builtin_amdgcn_readlane(start, 0), last_start = __builtin_amdgcn_readlane(start, 31);
     const int kv_end = (int)min(m0 + 32, p.N), qi = (int)row, lo = (int)start;
     if (tid == 0) spoilt = 0;
     __syncthreads();
@@ -207,8 +210,8 @@ __global__ __launch_bounds__(256, 1) void attn_fwd_short_kernel(FwdParams p) {
         l = __builtin_fmaf(stat[i][r][1], w[i], l);
     }
     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // NaN stays
-    int64_t rs, re;
-    p.seq.find(m0 + r, rs, re);
+    int rs, re;
+    seq.find((int)m0 + r, rs, re);
 #pragma unroll
     for (int j = 0; j < HDC / 32; ++j) {
         const int d = part * (HDC / 8) + 4 * j;
@@ -235,11 +238,14 @@ __global__ __launch_bounds__(256, 1) void attn_dq_short_kernel(BwdParams p) {
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
     const typename T::Lane lofs(lane);
+    __shared__ int32_t cu_lds[kSeqLds];
+    const Seqs seq(p.seq, cu_lds, tid, 256);
+    __syncthreads();
     const int head = (int)(blockIdx.x % p.Hq), kvh = head % p.Hkv, qh = kvh * p.G + head / p.Hkv;
     const int64_t m0 = 32 * (p.ntiles - 1 - blockIdx.x / p.Hq), row = m0 + (lane & 31);
-    int64_t start, end;
-    p.seq.find(row < p.N ? row : p.N - 1, start, end);
-    const int kv0 = __builtin_amdgcn_readlane((int)start, 0), last_start = __builtin_amdgcn_readlane((int)start, 31);
+    int start, end;
+    seq.find((int)min(row, p.N - 1), start, end);
+    const int kv0 = __builtin_amdgcn_readlane(start, 0), last_start = __builtin_amdgcn_readlane(start, 31);
     const int kv_end = (int)min(m0 + 32, p.N), qi = (int)row, lo = (int)start;
 
     const S *kb = static_cast<const S *>(p.k) + (int64_t)kvh * p.hd, *vb = static_cast<const S *>(p.v) + (int64_t)kvh * p.hd;
@@ -321,11 +327,14 @@ __global__ __launch_bounds__(256, 1) void attn_dkv_short_kernel(BwdParams p) {
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
     const typename T::Lane lofs(lane);
+    __shared__ int32_t cu_lds[kSeqLds];
+    const Seqs seq(p.seq, cu_lds, tid, 256);
+    __syncthreads();
     const int kvh = (int)(blockIdx.x % p.Hkv);
     const int64_t n0 = 32 * (int64_t)(blockIdx.x / p.Hkv), key = n0 + (lane & 31);
-    int64_t start, end;
-    p.seq.find(key < p.N ? key : p.N - 1, start, end);
-    const int first_end = __builtin_amdgcn_readlane((int)end, 0), q_end = __builtin_amdgcn_readlane((int)end, 31);
+    int start, end;
+    seq.find((int)min(key, p.N - 1), start, end);
+    const int first_end = __builtin_amdgcn_readlane(end, 0), q_end = __builtin_amdgcn_readlane(end, 31);
     const int q0 = (int)n0, ki = (int)key, hi = (int)end;
     if (tid == 0) spoilt = 0;
     __syncthreads();
@@ -397,8 +406,8 @@ __global__ __launch_bounds__(256, 1) void attn_dkv_short_kernel(BwdParams p) {
     __syncthreads();
     const int r = tid & 31, part = tid >> 5;
     if (n0 + r >= p.N) return;
-    int64_t rs, re;
-    p.seq.find(n0 + r, rs, re);
+    int rs, re;
+    seq.find((int)n0 + r, rs, re);
     const float w[4] = {1.f, 1.f, 1.f, 1.f};
 #pragma unroll
     for (int j = 0; j < HDC / 32; ++j) {
