@@ -6,13 +6,22 @@
 // Two kernels, no atomics, so every sum has one fixed order:
 //   attn_dq_kernel   block = 128 query rows of a head; walks the keys; also
 //                    forms delta and leaves it with log2(e) * lse in the
-//                    workspace for the second kernel;
+//                    workspace for the second kernel (bf16: delta from the
+//                    rounded o, corrected by the sum of the row's ds, which is
+//                    zero with the exact one);
 //   attn_dkv_kernel  block = 128 keys of a key head; walks the query rows of
 //                    every head of the group, so that the sum over the heads
 //                    stays in registers.
 // Forming the scores twice costs two of seven products; the alternative, one
 // walk with dq summed by atomics, would add each fp32 row of dq once per key
 // tile in an order that changes from run to run.
+//
+// Measured, bf16: the packed ~2B shape (32 heads of 128 over 8 key heads, 16384
+// tokens, 940 GFLOP of products) 548 us for dq, 725 us for dk and dv, 740
+// TFLOP/s over both; the ~150M shape (12 heads of 64, 8 x 2048 tokens, 180
+// GFLOP) 120 and 158 us, 650 TFLOP/s.  The matrix cores are busy for about 40%
+// of that, and exponentials, LDS fragment reads and the products' dependences
+// share the rest.  Few rows go to attn_short.hip.
 #include "attn_common.h"
 
 namespace dsc {
@@ -28,6 +37,7 @@ __global__ __launch_bounds__(256, (sizeof(typename E::store_t) == 2 ? 2 : 1)) vo
     using M = Mma<E>;
     using S = typename E::store_t;
     using frag = typename M::frag;
+    constexpr bool RND = sizeof(S) == 2;  // o was rounded
     constexpr int BN = kBT<E>, BM = 128, NS = BN / 32, KF = HDC / M::KC, DT = HDC / 32, PF = 16 / M::PR;
     __shared__ __align__(512) unsigned char k0s[BN * T::RB], v0s[BN * T::RB], k1s[BN * T::RB], v1s[BN * T::RB];
     __shared__ int flag;
@@ -67,17 +77,14 @@ __global__ __launch_bounds__(256, (sizeof(typename E::store_t) == 2 ? 2 : 1)) vo
     T::load_row(gf, static_cast<const S *>(p.dout) + (int64_t)qh * p.hd, os, row, p.N, p.hd, lane);
     const float delta = row_delta<T>(gf, static_cast<const S *>(p.o) + (int64_t)qh * p.hd, os, row, p.N, p.hd, lane);
     const float lse2 = row < p.N ? p.lse[(int64_t)qh * p.N + row] * kLog2e : 0.f;
-    if (h == 0 && row < p.N) {
-        p.delta[(int64_t)qh * p.N + row] = delta;
-        p.lse2[(int64_t)qh * p.N + row] = lse2;
-    }
 
     floatx16 acc[DT];
 #pragma unroll
     for (int d = 0; d < DT; ++d) acc[d] = zero16();
+    float off = 0.f;  // bf16: the sum of this row's ds (this half's), without the scale
 
     auto compute = [&](bool masked, int n0, bool dirty, const unsigned char *ks, const unsigned char *vs) __attribute__((always_inline)) {
-#pragma unroll
+#pragma unroll(RND && HDC > 64 ? 1 : NS)  // two copies of the walk's body spill with the sum of ds
         for (int j = 0; j < NS; ++j) {
             const typename T::Lane ln = lofs.fresh();
             floatx16 s = zero16(), dp = zero16();
@@ -94,6 +101,10 @@ __global__ __launch_bounds__(256, (sizeof(typename E::store_t) == 2 ? 2 : 1)) vo
                     const int key = n0 + 32 * j + res_row(i, h);
                     if (key > qi || key < lo) s[i] = 0.f;
                 }
+            }
+            if constexpr (RND) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) off += s[i];
             }
             // a key that is not finite leaves NaN in ds of the rows that see it, so no open pair is lost
             if (__builtin_expect(dirty, 0)) {
@@ -130,6 +141,18 @@ __global__ __launch_bounds__(256, (sizeof(typename E::store_t) == 2 ? 2 : 1)) vo
         step(n0, k0s, v0s, k1s, v1s);
         if (n0 + BN < kv_end) step(n0 + BN, k1s, v1s, k0s, v0s);
     }
+    // With delta exact, sum_j ds_ij = 0: what the sum comes to is delta's error,
+    // since o was rounded to bf16 before delta was formed from it.  The exact
+    // delta is what attn_dkv_kernel reads.  dq itself keeps the error's share,
+    // off * sum_j p_ij k_j (relative error 2.7e-3 at 1024 tokens, of which 1.7e-3
+    // is the rounding of dq): taking it back needs that sum, and over the last
+    // four key tiles alone it cost 18 % of this kernel for 2.4e-3.  Rows of few
+    // keys, where it weighs more, have it taken back in attn_dq_short_kernel.
+    off += other_half(off);
+    if (h == 0 && row < p.N) {
+        p.delta[(int64_t)qh * p.N + row] = delta + off;
+        p.lse2[(int64_t)qh * p.N + row] = lse2;
+    }
     T::store_row(acc, p.scale, static_cast<S *>(p.dq) + (int64_t)qh * p.hd, p.dqs, row, p.N, p.hd, lane);
 }
 
@@ -137,11 +160,11 @@ __global__ __launch_bounds__(256, (sizeof(typename E::store_t) == 2 ? 2 : 1)) vo
 // as nothing spills (spilled forms ran two to four times longer).  bf16 heads
 // over 64 channels get there (256 registers) with V in LDS, 32 query rows per
 // step and the phases of a step kept apart from the scheduler, which would
-// pull fragment reads forward (packed ~2B shape: 817 us; 64 keys per wave on
+// pull fragment reads forward (packed ~2B shape: 725 us; 64 keys per wave on
 // one wave per SIMD, which halves the LDS reads per product, 1300 us; K and V
 // in registers on one wave per SIMD 910 us).  Smaller heads have registers to
-// spare: K and V in registers, 64 rows per step (~150M shape: 180 us against
-// 220 us the other way).
+// spare: K and V in registers, 64 rows per step (~150M shape: 158 us; V in LDS
+// and 32 rows a step were a fifth slower).
 template <class E, int HDC>
 struct DkvCfg {
     static constexpr bool kBig = sizeof(typename E::store_t) == 2 && HDC > 64;
@@ -228,7 +251,6 @@ __global__ __launch_bounds__((64 * DkvCfg<E, HDC>::NW), (DkvCfg<E, HDC>::kOcc)) 
                 s = M::mul(T::read_row(qt, 32 * j, kc, ln), kf[kc], s);
             }
             frag pf[PF];
-            phase();
 #pragma unroll
             for (int i = 0; i < 16; i += 4) {
                 const float4 l = *reinterpret_cast<const float4 *>(lt + 32 * j + res_row(i, h));
@@ -246,19 +268,16 @@ __global__ __launch_bounds__((64 * DkvCfg<E, HDC>::NW), (DkvCfg<E, HDC>::kOcc)) 
             }
 #pragma unroll
             for (int f = 0; f < PF; ++f) pf[f] = M::pack(s, f);
-            phase();
 #pragma unroll
             for (int f = 0; f < PF; ++f)
 #pragma unroll
                 for (int d = 0; d < DT; ++d) dv[d] = M::mul(T::read_tr(gt, 32 * j, f, d, ln), pf[f], dv[d]);
-            phase();
 #pragma unroll
             for (int kc = 0; kc < KF; ++kc) {
                 const frag x = T::read_row(gt, 32 * j, kc, ln);
                 if constexpr (VL) dp = M::mul(x, T::read_row(vsh, 32 * wave, kc, ln), dp);
                 else dp = M::mul(x, vf[kc], dp);
             }
-            phase();
 #pragma unroll
             for (int i = 0; i < 16; i += 4) {
                 const float4 dl = *reinterpret_cast<const float4 *>(dt + 32 * j + res_row(i, h));
@@ -276,7 +295,6 @@ __global__ __launch_bounds__((64 * DkvCfg<E, HDC>::NW), (DkvCfg<E, HDC>::kOcc)) 
             }
 #pragma unroll
             for (int f = 0; f < PF; ++f) pf[f] = M::pack(s, f);
-            phase();
 #pragma unroll
             for (int f = 0; f < PF; ++f)
 #pragma unroll

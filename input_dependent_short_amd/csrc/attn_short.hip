@@ -8,6 +8,10 @@
 // barriers; two stages where they fit) and works as the long kernels do.  At
 // the end the waves' sums, brought to one maximum in the forward, are added in
 // LDS in a fixed order.  Four times the blocks, a quarter of the chain.
+//
+// The chain of dependent steps bounds it: 37 tokens of 12 heads of 64 take 8 us
+// with the launch; fp32, 6 heads of 64, 1501 ragged tokens, forward and
+// gradients 94 us.
 #include <algorithm>
 
 #include "attn_common.h"
@@ -234,7 +238,9 @@ __global__ __launch_bounds__(256, 1) void attn_dq_short_kernel(BwdParams p) {
     using frag = typename M::frag;
     using C = ShortCfg<E, HDC>;
     constexpr int KF = HDC / M::KC, DT = HDC / 32, PF = 16 / M::PR, SB = 2 * C::kTile;
+    constexpr bool RND = sizeof(S) == 2;  // o was rounded: delta's error is found (see attn_dq_kernel) and taken back
     __shared__ __align__(512) unsigned char st0[4 * SB], st1[C::kStages == 2 ? 4 * SB : 16];
+    __shared__ float offs[4][32];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
     const typename T::Lane lofs(lane);
@@ -255,13 +261,12 @@ __global__ __launch_bounds__(256, 1) void attn_dq_short_kernel(BwdParams p) {
     T::load_row(gf, static_cast<const S *>(p.dout) + (int64_t)qh * p.hd, os, row, p.N, p.hd, lane);
     const float delta = row_delta<T>(gf, static_cast<const S *>(p.o) + (int64_t)qh * p.hd, os, row, p.N, p.hd, lane);
     const float lse2 = row < p.N ? p.lse[(int64_t)qh * p.N + row] * kLog2e : 0.f;
-    if (wave == 0 && h == 0 && row < p.N) {
-        p.delta[(int64_t)qh * p.N + row] = delta;
-        p.lse2[(int64_t)qh * p.N + row] = lse2;
-    }
-    floatx16 acc[DT];
+    floatx16 acc[DT], mean[RND ? DT : 1];  // sums of ds k and of p k
 #pragma unroll
     for (int d = 0; d < DT; ++d) acc[d] = zero16();
+#pragma unroll
+    for (int d = 0; d < (RND ? DT : 1); ++d) mean[d] = zero16();
+    float off = 0.f;
     auto first = [&](int i) { return kv0 + 32 * (wave + 4 * i); };
 
     const int tiles = (kv_end - kv0 + 31) / 32;
@@ -281,25 +286,47 @@ __global__ __launch_bounds__(256, 1) void attn_dq_short_kernel(BwdParams p) {
 #pragma unroll
             for (int kc = 0; kc < KF; ++kc) dp = M::mul(T::read_row(ks + C::kTile, 0, kc, ln), gf[kc], dp);
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-                s[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], p.c2, -lse2)) * (dp[e] - delta);
+            for (int e = 0; e < 16; ++e) {
+                s[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], p.c2, -lse2));
+                dp[e] = s[e] * (dp[e] - delta);
+            }
             if (masked) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     const int key = n0 + res_row(e, h);
-                    if (key > qi || key < lo) s[e] = 0.f;
+                    if (key > qi || key < lo) s[e] = 0.f, dp[e] = 0.f;
                 }
                 wave_lds_fence();
                 own_dirty<T>(ks, lane);  // rows that see such a key have NaN in ds already
             }
 #pragma unroll
-            for (int f = 0; f < PF; ++f) {
-                const frag df = M::pack(s, f);
+            for (int e = 0; e < 16; ++e) off += dp[e];
 #pragma unroll
-                for (int d = 0; d < DT; ++d) acc[d] = M::mul(T::read_tr(ks, 0, f, d, ln), df, acc[d]);
+            for (int f = 0; f < PF; ++f) {
+                const frag df = M::pack(dp, f);
+#pragma unroll
+                for (int d = 0; d < DT; ++d) {
+                    const frag x = T::read_tr(ks, 0, f, d, ln);
+                    acc[d] = M::mul(x, df, acc[d]);
+                    if constexpr (RND) mean[d] = M::mul(x, M::pack(s, f), mean[d]);
+                }
             }
         });
 
+    off += other_half(off);
+    if (h == 0) offs[wave][lane] = off;
+    __syncthreads();
+    if constexpr (RND) {
+        off = (offs[0][lane & 31] + offs[1][lane & 31]) + (offs[2][lane & 31] + offs[3][lane & 31]);
+#pragma unroll
+        for (int d = 0; d < DT; ++d) acc[d] -= mean[d] * off;
+    } else {
+        off = 0.f;
+    }
+    if (wave == 0 && h == 0 && row < p.N) {
+        p.delta[(int64_t)qh * p.N + row] = delta + off;
+        p.lse2[(int64_t)qh * p.N + row] = lse2;
+    }
     park(acc, st0 + wave * SB, lane);
     __syncthreads();
     const int r = tid & 31, part = tid >> 5;
