@@ -17,7 +17,7 @@
 // tile in an order that changes from run to run.
 //
 // Measured, bf16: the packed ~2B shape (32 heads of 128 over 8 key heads, 16384
-// tokens, 940 GFLOP of products) 548 us for dq, 725 us for dk and dv, 740
+// tokens, 940 GFLOP of products) 533 us for dq, 715 us for dk and dv, 750
 // TFLOP/s over both; the ~150M shape (12 heads of 64, 8 x 2048 tokens, 180
 // GFLOP) 120 and 158 us, 650 TFLOP/s.  The matrix cores are busy for about 40%
 // of that, and exponentials, LDS fragment reads and the products' dependences
@@ -30,6 +30,11 @@ namespace {
 template <class E>
 constexpr int kBT = sizeof(typename E::store_t) == 2 ? 64 : 32;  // rows per walked tile
 
+// Rows of up to this many keys have the error that o's rounding leaves in dq
+// taken back (bf16).  Relative error of dq for sequences of 32 to 4096 tokens
+// with 0, 128, 512: 2.45 to 2.6e-3, 2.25 to 2.4e-3, the same; this kernel on the
+// packed ~2B shape 527, 533, 572 us.
+constexpr int kBack = 128;
 
 template <class E, int HDC>
 __global__ __launch_bounds__(256, (sizeof(typename E::store_t) == 2 ? 2 : 1)) void attn_dq_kernel(BwdParams p) {
@@ -143,12 +148,54 @@ __global__ __launch_bounds__(256, (sizeof(typename E::store_t) == 2 ? 2 : 1)) vo
     }
     // With delta exact, sum_j ds_ij = 0: what the sum comes to is delta's error,
     // since o was rounded to bf16 before delta was formed from it.  The exact
-    // delta is what attn_dkv_kernel reads.  dq itself keeps the error's share,
-    // off * sum_j p_ij k_j (relative error 2.7e-3 at 1024 tokens, of which 1.7e-3
-    // is the rounding of dq): taking it back needs that sum, and over the last
-    // four key tiles alone it cost 18 % of this kernel for 2.4e-3.  Rows of few
-    // keys, where it weighs more, have it taken back in attn_dq_short_kernel.
+    // delta is what attn_dkv_kernel reads.  dq's share, off * sum_j p_ij k_j, is
+    // taken back on a second walk by rows of up to kBack keys: there it weighs
+    // most, and of a long sequence only the first blocks walk again.
     off += other_half(off);
+    const int again = !RND ? kv_end : (int)m0 - kv0 < kBack ? kv0 : blk_last_start > (int)m0 ? (int)m0 : kv_end;
+    if (again < kv_end) {
+        const float back = qi - lo < kBack ? -off : 0.f;
+        const bool any = __builtin_amdgcn_ballot_w64(qi - lo < kBack) != 0;
+        auto fetch = [&](int n0, unsigned char *ks) __attribute__((always_inline)) {
+            if (n0 < kv_end) T::template load<BN, 4>(ks, kb, p.ks, n0, kv_end, p.hd, wave, lane);
+        };
+        auto take_back = [&](int n0, const unsigned char *ks, unsigned char *kn) __attribute__((always_inline)) {
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            fetch(n0 + BN, kn);
+            if (!any) return;
+#pragma clang loop unroll(disable)
+            for (int j = 0; j < NS; ++j) {
+                if (n0 + 32 * j > wlast || n0 + 32 * j + 32 <= wfirst_key) continue;
+                const typename T::Lane ln = lofs.fresh();
+                const unsigned char *kj = ks + 32 * j * T::RB;
+                floatx16 s = zero16();
+#pragma unroll
+                for (int kc = 0; kc < KF; ++kc) s = M::mul(T::read_row(kj, 0, kc, ln), qf[kc], s);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int key = n0 + 32 * j + res_row(i, h);
+                    s[i] = back * __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], p.c2, -lse2));
+                    if (key > qi || key < lo) s[i] = 0.f;
+                }
+#pragma unroll
+                for (int f = 0; f < PF; ++f) {
+                    const frag df = M::pack(s, f);
+#pragma unroll
+                    for (int d = 0; d < DT; ++d) acc[d] = M::mul(T::finite(T::read_tr(kj, 0, f, d, ln)), df, acc[d]);
+                }
+            }
+        };
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();  // every wave is done with the first walk's tiles
+        asm volatile("" ::: "memory");
+        fetch(again, k0s);
+        for (int n0 = again; n0 < kv_end; n0 += 2 * BN) {
+            take_back(n0, k0s, k1s);
+            if (n0 + BN < kv_end) take_back(n0 + BN, k1s, k0s);
+        }
+    }
     if (h == 0 && row < p.N) {
         p.delta[(int64_t)qh * p.N + row] = delta + off;
         p.lse2[(int64_t)qh * p.N + row] = lse2;
@@ -160,7 +207,7 @@ __global__ __launch_bounds__(256, (sizeof(typename E::store_t) == 2 ? 2 : 1)) vo
 // as nothing spills (spilled forms ran two to four times longer).  bf16 heads
 // over 64 channels get there (256 registers) with V in LDS, 32 query rows per
 // step and the phases of a step kept apart from the scheduler, which would
-// pull fragment reads forward (packed ~2B shape: 725 us; 64 keys per wave on
+// pull fragment reads forward (packed ~2B shape: 715 us; 64 keys per wave on
 // one wave per SIMD, which halves the LDS reads per product, 1300 us; K and V
 // in registers on one wave per SIMD 910 us).  Smaller heads have registers to
 // spare: K and V in registers, 64 rows per step (~150M shape: 158 us; V in LDS
