@@ -199,6 +199,35 @@ def test_gradient_rows_that_a_key_must_not_see(dtype, bad, Hq, Hkv):
     assert torch.equal(got["dq"][0, at, 0], clean["dq"][0, at, 0]) and not torch.isfinite(got["dq"][0, at, 1]).any()
 
 
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("B,T,heads,n", [(3, 96, 2, 96), (42, 96, 12, 96), (8, 2048, 12, 2048)])
+def test_values_far_from_zero_lose_no_gradient(B, T, heads, n, hd):
+    """Values with a common part of 8: o, rounded to bf16, is off by 8 * 2^-9 or so, and a delta formed from it would
+    miss by 1.3% of <g, v_j - o> in every pair of the row.  What may remain of dk, and of dq where the rows have few
+    keys: one rounding of ds or p and one of the result, each of at most 2^-8 and evenly spread, hence of at most
+    2^-8 / sqrt(3) in the root mean square; both and the small rest come to less than 2^-8.  Three sizes: few rows,
+    many short sequences, long ones (dk)."""
+    r = np.random.default_rng(23)
+    q, k, v, g = (torch.from_numpy(r.standard_normal((B, T, heads, hd), dtype=np.float32)) for _ in range(4))
+    q, k, v, g = (t.to(torch.bfloat16).cuda() for t in (q, k, v + 8.0, g))
+    scale = hd ** -0.5
+    out = run(q, k, v, g, None, scale, "dense")
+    sums = {"dq": [0.0, 0.0], "dk": [0.0, 0.0]}
+    later = torch.ones(n, n, dtype=torch.bool, device="cuda").triu(1)
+    for b in (0, B - 1):
+        for a in (0, heads - 1):
+            Q, K, V, G = (t[b, :, a].double() for t in (q, k, v, g))
+            P = (Q @ K.t() * scale).masked_fill(later, -float("inf")).softmax(1)
+            ds = scale * P * (G @ V.t() - (G * (P @ V)).sum(1, keepdim=True))
+            for name, want in (("dq", ds @ K), ("dk", ds.t() @ Q)):
+                sums[name][0] += float((out[name][b, :, a].double() - want).square().sum())
+                sums[name][1] += float(want.square().sum())
+    for name in ("dq", "dk") if n <= 128 else ("dk",):
+        err = (sums[name][0] / sums[name][1]) ** 0.5
+        say(f"    {name}: relative error {err:.2e}")
+        assert err < 2.0 ** -8, f"{name}: {err:.3g}"
+
+
 @pytest.mark.parametrize("Hq,Hkv", [(8, 2), (64, 32)])
 def test_same_bits_every_time(Hq, Hkv):
     _, q, k, v = qkv(2, 400, Hq, Hkv, 128, "bf16", 41)
