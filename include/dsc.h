@@ -509,7 +509,8 @@ DSC_API dsc_status dsc_state_from_prefill(void *stream, int dtype, int64_t B, in
  *              1/sqrt(head_dim)).
  * Scores, softmax statistics and sums are fp32; with DSC_BF16 the
  * probabilities and score gradients are rounded to bf16 as operands of the
- * matrix cores, and each output once.  These calls also take offsets that
+ * matrix cores, and each output once; the backward takes out what the rounding
+ * of o leaves in dk, and in dq for rows of up to 128 keys.  These calls also take offsets that
  * are equal (sequences without tokens).
  */
 
@@ -531,7 +532,8 @@ DSC_API dsc_status dsc_attn_fwd(void *stream, int dtype, int64_t B, int64_t T, i
                                 float scale, void *o, float *lse);
 
 /* Bytes of device workspace dsc_attn_bwd needs (0 for invalid sizes): two
- * fp32 values per query head and token. */
+ * fp32 values per query head and token, and for few tokens the partial sums of
+ * dk and dv (at most 8 MiB more on 256 compute units). */
 DSC_API size_t dsc_attn_bwd_workspace_size(int dtype, int64_t B, int64_t T, int32_t Hq, int32_t Hkv,
                                            int32_t head_dim);
 

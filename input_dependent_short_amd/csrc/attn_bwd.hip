@@ -399,13 +399,18 @@ void dispatch(const BwdParams &p, hipStream_t s, bool dq, bool dkv) {
 
 }  // namespace
 
-size_t attn_bwd_workspace(int64_t N, int32_t Hq) { return 2 * sizeof(float) * (size_t)N * (size_t)Hq; }
+size_t attn_bwd_workspace(int64_t N, int32_t Hq, int32_t Hkv, int32_t hd) {
+    const int32_t parts = attn_dkv_max_parts(N, Hkv);
+    const size_t rows = (2 * (size_t)N * Hq + 3) / 4 * 4;  // what follows is 16-byte aligned
+    return sizeof(float) * (rows + (parts > 1 ? 2 * (size_t)parts * N * Hkv * hd : 0));
+}
 
 hipError_t attn_bwd(const AttnProblem &a, hipStream_t s) {
     float *delta = static_cast<float *>(a.ws);
     BwdParams p{a.q, a.k, a.v, a.o, a.dout, a.lse, a.dq, a.dk, a.dv, delta, delta + a.N * a.Hq,
                 SeqMap{a.cu, a.n_seqs, a.T}, a.N, a.qs, a.ks, a.vs, a.dqs, a.dks, a.dvs, a.Hq, a.Hkv,
-                a.Hq / a.Hkv, a.hd, a.scale, a.scale * kLog2e, (a.N + 127) / 128, false};
+                a.Hq / a.Hkv, a.hd, a.scale, a.scale * kLog2e, (a.N + 127) / 128, false,
+                delta + (2 * a.N * a.Hq + 3) / 4 * 4, 1};
     p.order = p.ntiles * p.Hkv > device_cus();  // with a block or less per CU all start at once
     const bool few_q = attn_few_rows(p.ntiles * p.Hq, p.seq, p.N),
                few_k = attn_few_rows(p.ntiles * p.Hkv, p.seq, p.N);

@@ -487,7 +487,9 @@ struct BwdParams {
     int32_t Hq, Hkv, G, hd;
     float scale, c2;
     int64_t ntiles;
-    bool order;  // heaviest tiles first
+    bool order;   // heaviest tiles first
+    float *sums;  // workspace (parts, dk and dv, N, Hkv, hd): attn_dkv_short's blocks that share keys
+    int32_t parts;
 };
 
 // attn_short.hip: the same results for inputs of few rows; blocks counts the
@@ -496,6 +498,7 @@ bool attn_few_rows(int64_t blocks, const SeqMap &seq, int64_t N);
 void attn_fwd_short(FwdParams p, Dtype dt, hipStream_t s);
 void attn_dq_short(BwdParams p, Dtype dt, hipStream_t s);
 void attn_dkv_short(BwdParams p, Dtype dt, hipStream_t s);
+int32_t attn_dkv_max_parts(int64_t N, int32_t Hkv);
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;

@@ -7,11 +7,14 @@
 // 32 goes to wave i % 4, which loads it into LDS stages of its own (no
 // barriers; two stages where they fit) and works as the long kernels do.  At
 // the end the waves' sums, brought to one maximum in the forward, are added in
-// LDS in a fixed order.  Four times the blocks, a quarter of the chain.
+// LDS in a fixed order.  Four times the blocks, a quarter of the chain.  For dk
+// and dv, which walk the rows of every head of the group, several blocks share
+// a walk where the device has room for them; their fp32 sums go to the workspace
+// and a second launch adds them in a fixed order.
 //
 // The chain of dependent steps bounds it: 37 tokens of 12 heads of 64 take 8 us
-// with the launch; fp32, 6 heads of 64, 1501 ragged tokens, forward and
-// gradients 94 us.
+// with the launch; fp32, 6 heads over 2 of 64, 1501 ragged tokens, forward and
+// gradients 74 us.
 #include <algorithm>
 
 #include "attn_common.h"
@@ -89,8 +92,8 @@ __device__ __forceinline__ void join4(const unsigned char *st, int stage, int r,
 }
 
 // As Tile::add_nonfinite, for four channels of one row.
-template <class E, class Open>
-__device__ void add_nonfinite4(typename E::store_t *dst, const typename E::store_t *src, int64_t stride, int r0, int r1,
+template <class E, class D, class Open>
+__device__ void add_nonfinite4(D *dst, const typename E::store_t *src, int64_t stride, int r0, int r1,
                                const Open &open) {
     for (int c = 0; c < 4; ++c) {
         float a = 0.f;
@@ -101,9 +104,8 @@ __device__ void add_nonfinite4(typename E::store_t *dst, const typename E::store
             if ((__float_as_uint(x) & 0x7f800000u) == 0x7f800000u && open(r)) a += x, any = true;
         }
         if (!any) continue;
-        a += load_elem<E>(dst + c);
-        if constexpr (sizeof(typename E::store_t) == 4) dst[c] = a;
-        else dst[c] = to_bf16(a);
+        if constexpr (sizeof(D) == 4) dst[c] += a;
+        else dst[c] = to_bf16(load_elem<E>(dst + c) + a);
     }
 }
 
@@ -357,8 +359,8 @@ __global__ __launch_bounds__(256, 1) void attn_dkv_short_kernel(BwdParams p) {
     __shared__ int32_t cu_lds[kSeqLds];
     const Seqs seq(p.seq, cu_lds, tid, 256);
     __syncthreads();
-    const int kvh = (int)(blockIdx.x % p.Hkv);
-    const int64_t n0 = 32 * (int64_t)(blockIdx.x / p.Hkv), key = n0 + (lane & 31);
+    const int share = (int)(blockIdx.x % p.parts), kvh = (int)(blockIdx.x / p.parts % p.Hkv);
+    const int64_t n0 = 32 * (int64_t)(blockIdx.x / p.parts / p.Hkv), key = n0 + (lane & 31);
     int start, end;
     seq.find((int)min(key, p.N - 1), start, end);
     const int first_end = __builtin_amdgcn_readlane(end, 0), q_end = __builtin_amdgcn_readlane(end, 31);
@@ -374,12 +376,13 @@ __global__ __launch_bounds__(256, 1) void attn_dkv_short_kernel(BwdParams p) {
 #pragma unroll
     for (int d = 0; d < DT; ++d) dk[d] = zero16(), dv[d] = zero16();
     const int nt = (q_end - q0 + 31) / 32, total = nt * p.G;
+    const int first = wave + 4 * share, every = 4 * p.parts;
     auto tile_masked = [&](int m0) { return m0 < (int)n0 + 31 || m0 + 32 > first_end; };
 
     walk<C::kStages, 2 * C::PER + 2>(
-        (total + 3 - wave) / 4, st0 + wave * SB, st1 + (C::kStages == 2 ? wave * SB : 0),
+        (total + every - 1 - first) / every, st0 + wave * SB, st1 + (C::kStages == 2 ? wave * SB : 0),
         [&](int i, unsigned char *st) __attribute__((always_inline)) {
-            const int it = wave + 4 * i, g = it / nt, m0 = q0 + (it - g * nt) * 32;
+            const int it = first + every * i, g = it / nt, m0 = q0 + (it - g * nt) * 32;
             const int64_t qh = (int64_t)kvh * p.G + g;
             T::template load<32, 1>(st, static_cast<const S *>(p.q) + qh * p.hd, p.qs, m0, q_end, p.hd, 0, lane);
             T::template load<32, 1>(st + C::kTile, static_cast<const S *>(p.dout) + qh * p.hd, os, m0, q_end, p.hd, 0, lane);
@@ -389,7 +392,7 @@ __global__ __launch_bounds__(256, 1) void attn_dkv_short_kernel(BwdParams p) {
         },
         [&](int i, unsigned char *qt) __attribute__((always_inline)) {
             unsigned char *gt = qt + C::kTile;
-            const int it = wave + 4 * i, g = it / nt, m0 = q0 + (it - g * nt) * 32;
+            const int it = first + every * i, g = it / nt, m0 = q0 + (it - g * nt) * 32;
             const float *lt = reinterpret_cast<const float *>(qt + LO), *dt = reinterpret_cast<const float *>(qt + DO);
             const bool masked = tile_masked(m0);
             if (masked) {
@@ -440,14 +443,45 @@ __global__ __launch_bounds__(256, 1) void attn_dkv_short_kernel(BwdParams p) {
     for (int j = 0; j < HDC / 32; ++j) {
         const int d = part * (HDC / 8) + 4 * j;
         if (d >= p.hd) continue;
+        auto spoil = [&](auto *dst) __attribute__((always_inline)) {
+            if (__builtin_expect(spoilt, 0))
+                for (int g = 0; g < p.G; ++g)
+                    add_nonfinite4<E>(dst, static_cast<const S *>(p.dout) + ((int64_t)kvh * p.G + g) * p.hd + d, os, q0, q_end,
+                                      [&](int t) { return t >= (int)n0 + r && t < re && tile_masked(t - (t - q0) % 32); });
+        };
+        if (p.parts > 1) {  // adding what is not finite once per part changes nothing
+            float *dkp = p.sums + ((2 * (int64_t)share * p.N + n0 + r) * p.Hkv + kvh) * p.hd + d;
+            float *dvp = dkp + p.N * p.Hkv * p.hd;
+            join4<F32>(st0, SB, r, d, w, 1.f, dkp);
+            join4<F32>(vst, SB, r, d, w, 1.f, dvp);
+            spoil(dvp);
+            continue;
+        }
         S *dvp = static_cast<S *>(p.dv) + (n0 + r) * p.dvs + (int64_t)kvh * p.hd + d;
         join4<E>(st0, SB, r, d, w, p.scale, static_cast<S *>(p.dk) + (n0 + r) * p.dks + (int64_t)kvh * p.hd + d);
         join4<E>(vst, SB, r, d, w, 1.f, dvp);
-        if (__builtin_expect(spoilt, 0))
-            for (int g = 0; g < p.G; ++g)
-                add_nonfinite4<E>(dvp, static_cast<const S *>(p.dout) + ((int64_t)kvh * p.G + g) * p.hd + d, os, q0, q_end,
-                                  [&](int t) { return t >= (int)n0 + r && t < re && tile_masked(t - (t - q0) % 32); });
+        spoil(dvp);
     }
+}
+
+// dk and dv from the parts' sums, four channels per thread.
+template <class E>
+__global__ __launch_bounds__(256) void attn_dkv_join_kernel(BwdParams p) {
+    using S = typename E::store_t;
+    const int64_t at = 4 * (256 * (int64_t)blockIdx.x + threadIdx.x), row = (int64_t)p.Hkv * p.hd, all = p.N * row;
+    if (at >= all) return;
+    const int64_t n = at / row, c = at - n * row;
+    auto one = [&](int which, float mul, S *dst) __attribute__((always_inline)) {
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < p.parts; ++i) {
+            const float4 x = *reinterpret_cast<const float4 *>(p.sums + (2 * i + which) * all + at);
+            a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
+        }
+        if constexpr (sizeof(S) == 4) *reinterpret_cast<float4 *>(dst) = make_float4(a.x * mul, a.y * mul, a.z * mul, a.w * mul);
+        else *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(a.x * mul, a.y * mul), pack_bf16x2(a.z * mul, a.w * mul));
+    };
+    one(0, p.scale, static_cast<S *>(p.dk) + n * p.dks + c);
+    one(1, 1.f, static_cast<S *>(p.dv) + n * p.dvs + c);
 }
 
 // One launch of KERNEL<E, HDC> with a block per 32 rows and head.
@@ -464,7 +498,13 @@ void fwd(const FwdParams &p, hipStream_t s) { DSC_ATTN_SHORT(attn_fwd_short_kern
 template <class E>
 void dq(const BwdParams &p, hipStream_t s) { DSC_ATTN_SHORT(attn_dq_short_kernel, p, p.Hq); }
 template <class E>
-void dkv(const BwdParams &p, hipStream_t s) { DSC_ATTN_SHORT(attn_dkv_short_kernel, p, p.Hkv); }
+void dkv(const BwdParams &p, hipStream_t s) {
+    DSC_ATTN_SHORT(attn_dkv_short_kernel, p, p.Hkv * p.parts);
+    if (p.parts > 1) {
+        const int64_t threads = p.N * p.Hkv * p.hd / 4;
+        hipLaunchKernelGGL((attn_dkv_join_kernel<E>), dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, p);
+    }
+}
 
 }  // namespace
 
@@ -492,8 +532,26 @@ void attn_dq_short(BwdParams p, Dtype dt, hipStream_t s) {
     else dq<F32>(p, s);
 }
 
+// Blocks of dk and dv that share the walk of 32 keys: as many as fill the
+// device once, at most kMaxParts, as long as each has 8 tiles (fp32: 4) of the mean
+// sequence to walk (one / so many blocks, dq included, us: fp32, 6 heads over 2
+// of 64, 1501 ragged tokens 78.5 / 56.5; 4 over 1 of 128, 700 tokens 241 / 94;
+// bf16, 8 over 1 of 128, 2048 tokens 274 / 100; 2 over 1 of 64, 4000 tokens
+// 100 / 72).  Filling it twice costs where there is less to share (bf16, 12
+// heads of 64, 512 tokens 18 / 22), and so do half the tiles per block in bf16
+// (4 x 300 tokens, 2 heads of 128, 28 / 29; fp32 gains, 8 heads of 64, 300
+// tokens, 38.0 / 36.6).
+constexpr int64_t kMaxParts = 8;
+int32_t attn_dkv_max_parts(int64_t N, int32_t Hkv) {
+    const int64_t blocks = std::max<int64_t>(1, (N + 31) / 32 * Hkv);
+    return (int32_t)std::min(kMaxParts, std::max<int64_t>(1, device_cus() / blocks));
+}
+
 void attn_dkv_short(BwdParams p, Dtype dt, hipStream_t s) {
     p.ntiles = (p.N + 31) / 32;
+    const int64_t mean = p.seq.cu ? p.N / std::max(p.seq.n_seqs, 1) : p.seq.T;
+    const int64_t steps = dt == Dtype::BF16 ? 8 : 4;  // least tiles per block
+    p.parts = (int32_t)std::min<int64_t>(attn_dkv_max_parts(p.N, p.Hkv), std::max<int64_t>(1, p.G * ((mean + 31) / 32) / steps));
     if (dt == Dtype::BF16) dkv<BF16>(p, s);
     else dkv<F32>(p, s);
 }

@@ -767,7 +767,7 @@ dsc_status dsc_attn_fwd(void *stream, int dtype, int64_t B, int64_t T, int32_t H
 
 size_t dsc_attn_bwd_workspace_size(int dtype, int64_t B, int64_t T, int32_t Hq, int32_t Hkv, int32_t head_dim) {
     if (check_attn(dtype, B, T, Hq, Hkv, head_dim, nullptr, 0) != DSC_SUCCESS) return 0;
-    return dsc::attn_bwd_workspace(B * T, Hq);
+    return dsc::attn_bwd_workspace(B * T, Hq, Hkv, head_dim);
 }
 
 dsc_status dsc_attn_bwd(void *stream, int dtype, int64_t B, int64_t T, int32_t Hq, int32_t Hkv, int32_t head_dim,
@@ -789,7 +789,7 @@ dsc_status dsc_attn_bwd(void *stream, int dtype, int64_t B, int64_t T, int32_t H
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse) || !aligned16(dout) ||
         !aligned16(dq) || !aligned16(dk) || !aligned16(dv) || !aligned16(workspace))
         return fail(DSC_ERR_ALIGNMENT, "pointers must be 16-byte aligned");
-    const size_t need = dsc::attn_bwd_workspace(B * T, Hq);
+    const size_t need = dsc::attn_bwd_workspace(B * T, Hq, Hkv, head_dim);
     if (!workspace || workspace_bytes < need)
         return fail(DSC_ERR_WORKSPACE, "workspace of %zu bytes required (got %zu)", need, workspace ? workspace_bytes : 0);
     const size_t es = esize(dtype), N = (size_t)(B * T);

@@ -194,7 +194,7 @@ struct AttnProblem {
     void *ws;  // attn_bwd_workspace bytes
 };
 hipError_t attn_fwd(const AttnProblem &p, hipStream_t s);
-size_t attn_bwd_workspace(int64_t N, int32_t Hq);
+size_t attn_bwd_workspace(int64_t N, int32_t Hq, int32_t Hkv, int32_t hd);
 hipError_t attn_bwd(const AttnProblem &p, hipStream_t s);
 
 // A paged cache: k, v (num_pages, Hkv, page, hd), pages (S, max_pages) int32.
