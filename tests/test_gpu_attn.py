@@ -239,6 +239,27 @@ def test_same_bits_every_time(Hq, Hkv):
             assert torch.equal(a[n], b[n]), n
 
 
+# groups so large that several blocks share the walk of 32 keys
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_what_a_row_must_not_see_in_shared_walks(dtype, bad):
+    test_what_a_row_must_not_see(dtype, bad, 32, 2)
+    test_gradient_rows_that_a_key_must_not_see(dtype, bad, 32, 2)
+
+
+@pytest.mark.parametrize("dtype,B,T,Hq,Hkv,hd,lens", [
+    ("bf16", 1, 700, 8, 1, 128, None), ("bf16", 1, 601, 12, 2, 96, [1, 0, 400, 33, 167]), ("bf16", 2, 130, 16, 1, 40, None),
+    ("fp32", 1, 500, 4, 1, 128, None), ("fp32", 1, 333, 14, 2, 20, [32, 1, 300])])
+def test_shared_walks(dtype, B, T, Hq, Hkv, hd, lens):
+    test_prompt_and_gradients(dtype, B, T, Hq, Hkv, hd, lens, "packed")
+    _, q, k, v = qkv(B, T, Hq, Hkv, hd, dtype, 43)
+    g = torch.randn(B, T, Hq, hd, device="cuda").to(q.dtype)
+    a = {n: t.clone() for n, t in run(q, k, v, g, cu_of(lens), 0.1).items()}
+    b = run(q, k, v, g, cu_of(lens), 0.1)
+    for n in a:
+        assert torch.equal(a[n], b[n]), n
+
+
 def test_without_lse_and_on_another_stream():
     _, q, k, v = qkv(1, 333, 4, 4, 64, "bf16", 51)
     want = run(q, k, v, None, None, 0.125)["o"]
