@@ -400,7 +400,7 @@ void dispatch(const BwdParams &p, hipStream_t s, bool dq, bool dkv) {
 }  // namespace
 
 size_t attn_bwd_workspace(int64_t N, int32_t Hq, int32_t Hkv, int32_t hd) {
-    const int32_t parts = attn_dkv_max_parts(N, Hkv);
+    const int32_t parts = attn_dkv_max_parts(N, Hkv, Hq / Hkv);
     const size_t rows = (2 * (size_t)N * Hq + 3) / 4 * 4;  // what follows is 16-byte aligned
     return sizeof(float) * (rows + (parts > 1 ? 2 * (size_t)parts * N * Hkv * hd : 0));
 }

@@ -498,7 +498,7 @@ bool attn_few_rows(int64_t blocks, const SeqMap &seq, int64_t N);
 void attn_fwd_short(FwdParams p, Dtype dt, hipStream_t s);
 void attn_dq_short(BwdParams p, Dtype dt, hipStream_t s);
 void attn_dkv_short(BwdParams p, Dtype dt, hipStream_t s);
-int32_t attn_dkv_max_parts(int64_t N, int32_t Hkv);
+int32_t attn_dkv_max_parts(int64_t N, int32_t Hkv, int32_t G);
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;

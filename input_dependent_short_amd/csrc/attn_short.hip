@@ -14,7 +14,7 @@
 //
 // The chain of dependent steps bounds it: 37 tokens of 12 heads of 64 take 8 us
 // with the launch; fp32, 6 heads over 2 of 64, 1501 ragged tokens, forward and
-// gradients 74 us.
+// gradients 77 us.
 #include <algorithm>
 
 #include "attn_common.h"
@@ -533,25 +533,29 @@ void attn_dq_short(BwdParams p, Dtype dt, hipStream_t s) {
 }
 
 // Blocks of dk and dv that share the walk of 32 keys: as many as fill the
-// device once, at most kMaxParts, as long as each has 8 tiles (fp32: 4) of the mean
+// device once, at most kMaxParts, as long as each has kSteps tiles of the mean
 // sequence to walk (one / so many blocks, dq included, us: fp32, 6 heads over 2
-// of 64, 1501 ragged tokens 78.5 / 56.5; 4 over 1 of 128, 700 tokens 241 / 94;
-// bf16, 8 over 1 of 128, 2048 tokens 274 / 100; 2 over 1 of 64, 4000 tokens
+// of 64, 1501 ragged tokens 82 / 61; 4 over 1 of 128, 700 tokens 241 / 94;
+// bf16, 8 over 1 of 128, 2048 tokens 270 / 119; 2 over 1 of 64, 4000 tokens
 // 100 / 72).  Filling it twice costs where there is less to share (bf16, 12
 // heads of 64, 512 tokens 18 / 22), and so do half the tiles per block in bf16
 // (4 x 300 tokens, 2 heads of 128, 28 / 29; fp32 gains, 8 heads of 64, 300
 // tokens, 38.0 / 36.6).
 constexpr int64_t kMaxParts = 8;
-int32_t attn_dkv_max_parts(int64_t N, int32_t Hkv) {
-    const int64_t blocks = std::max<int64_t>(1, (N + 31) / 32 * Hkv);
-    return (int32_t)std::min(kMaxParts, std::max<int64_t>(1, device_cus() / blocks));
+template <class E>
+constexpr int64_t kSteps = sizeof(typename E::store_t) == 2 ? 8 : 4;
+static int32_t dkv_parts(int64_t N, int32_t Hkv, int32_t G, int64_t mean, int64_t steps) {
+    const int64_t blocks = std::max<int64_t>(1, (N + 31) / 32 * Hkv), tiles = G * ((mean + 31) / 32);
+    return (int32_t)std::max<int64_t>(1, std::min({kMaxParts, device_cus() / blocks, tiles / steps}));
 }
+
+// Whatever the type and the sequences; for the size of the workspace.
+int32_t attn_dkv_max_parts(int64_t N, int32_t Hkv, int32_t G) { return dkv_parts(N, Hkv, G, N, kSteps<F32>); }
 
 void attn_dkv_short(BwdParams p, Dtype dt, hipStream_t s) {
     p.ntiles = (p.N + 31) / 32;
     const int64_t mean = p.seq.cu ? p.N / std::max(p.seq.n_seqs, 1) : p.seq.T;
-    const int64_t steps = dt == Dtype::BF16 ? 8 : 4;  // least tiles per block
-    p.parts = (int32_t)std::min<int64_t>(attn_dkv_max_parts(p.N, p.Hkv), std::max<int64_t>(1, p.G * ((mean + 31) / 32) / steps));
+    p.parts = dkv_parts(p.N, p.Hkv, p.G, mean, dt == Dtype::BF16 ? kSteps<BF16> : kSteps<F32>);
     if (dt == Dtype::BF16) dkv<BF16>(p, s);
     else dkv<F32>(p, s);
 }
